@@ -60,6 +60,16 @@ EXPORTS = ("gemm_create", "gemm_destroy", "gemm_check_args", "gemm_run", "gemm_r
            "gemm_wall_clock_khz", "gemm_probe_bandwidth", "gemm_run_ws", "gemm_run_ws_kernel",
            "gemm_workspace_bytes", "gemm_run_noalloc", "gemm_kernel_workspace_bytes")
 
+# gemm_grouped_kernel_t
+GEMM_GROUPED_AUTO = 0
+GEMM_GROUPED_ANY = 1
+GROUPED_KERNEL_NAME = {0: "auto", 1: "any"}
+
+# Every symbol include/gemm_grouped.h declares.
+GROUPED_EXPORTS = ("gemm_run_grouped", "gemm_run_grouped_wgrad", "gemm_run_i8",
+                   "gemm_run_grouped_i8", "gemm_quantize_rows", "gemm_check_args_grouped",
+                   "gemm_check_args_grouped_wgrad", "gemm_check_args_quantize_rows")
+
 # libgemm.so must resolve its libamdhip64.so.7 dependency to the HIP runtime instance that owns
 # the caller's device pointers and streams.  PyTorch ships its own runtime (soname
 # libamdhip64.so.7, but its libraries ask for plain "libamdhip64.so"): if libgemm.so were loaded
@@ -138,6 +148,29 @@ _lib.gemm_wall_clock_khz.argtypes = [_vp]
 _lib.gemm_wall_clock_khz.restype = _int
 _lib.gemm_probe_bandwidth.argtypes = [_vp, _vp, _vp, _vp, _i64, _vp]
 _lib.gemm_probe_bandwidth.restype = _int
+_GRP = [_i64, _vp, _i64, _i64, _i64, _int]  # groups, offsets, M, N, K, transB
+_lib.gemm_run_grouped.argtypes = [_vp, _int, _vp] + _GRP + [_f32, _vp, _i64, _vp, _i64, _i64, _f32,
+                                                            _vp, _i64, _int, _u32, _vp]
+_lib.gemm_run_grouped.restype = _int
+_lib.gemm_run_grouped_wgrad.argtypes = [_vp, _int, _vp] + _GRP + [_f32, _vp, _i64, _vp, _i64, _f32,
+                                                                  _vp, _i64, _i64, _int, _int, _vp]
+_lib.gemm_run_grouped_wgrad.restype = _int
+_lib.gemm_run_i8.argtypes = [_vp, _int, _vp, _i64, _i64, _i64, _int, _f32, _vp, _i64, _vp, _vp,
+                             _i64, _vp, _f32, _vp, _i64, _int, _u32, _vp]
+_lib.gemm_run_i8.restype = _int
+_lib.gemm_run_grouped_i8.argtypes = [_vp, _int, _vp] + _GRP + [_f32, _vp, _i64, _vp, _vp, _i64, _i64,
+                                                               _vp, _f32, _vp, _i64, _int, _u32, _vp]
+_lib.gemm_run_grouped_i8.restype = _int
+_lib.gemm_quantize_rows.argtypes = [_vp, _vp, _i64, _i64, _vp, _i64, _int, _vp, _i64, _vp]
+_lib.gemm_quantize_rows.restype = _int
+_lib.gemm_check_args_grouped.argtypes = _GRP + [_vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _int,
+                                                _int, _int, _u32, _vp]
+_lib.gemm_check_args_grouped.restype = _int
+_lib.gemm_check_args_grouped_wgrad.argtypes = _GRP + [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _int,
+                                                      _int, _vp]
+_lib.gemm_check_args_grouped_wgrad.restype = _int
+_lib.gemm_check_args_quantize_rows.argtypes = [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp]
+_lib.gemm_check_args_quantize_rows.restype = _int
 _lib.gemm_status_string.argtypes = [_int]
 _lib.gemm_status_string.restype = ctypes.c_char_p
 
@@ -310,6 +343,58 @@ def gemm_probe_bandwidth(handle, stream, src, dst, nbytes, sink) -> int:
     return _lib.gemm_probe_bandwidth(handle, stream, src, dst, nbytes, sink)
 
 
+def gemm_run_grouped(handle, kernel, stream, groups, offsets, M, N, K, transB, alpha, A, lda, B,
+                     ldb, stride_b, beta, C, ldc, dtype, epilogue, bias) -> int:
+    """Raw grouped product (include/gemm_grouped.h): returns the status code (no exception)."""
+    return _lib.gemm_run_grouped(handle, kernel, stream, groups, offsets, M, N, K, transB, alpha, A,
+                                 lda, B, ldb, stride_b, beta, C, ldc, dtype, epilogue, bias)
+
+
+def gemm_run_grouped_wgrad(handle, kernel, stream, groups, offsets, M, N, K, transB, alpha, A, lda,
+                           D, ldd, beta, C, ldc, stride_c, dtype, c_type, dbias) -> int:
+    """Raw grouped weight gradient: returns the status code (no exception)."""
+    return _lib.gemm_run_grouped_wgrad(handle, kernel, stream, groups, offsets, M, N, K, transB,
+                                       alpha, A, lda, D, ldd, beta, C, ldc, stride_c, dtype, c_type,
+                                       dbias)
+
+
+def gemm_run_i8(handle, kernel, stream, M, N, K, transB, alpha, A, lda, sa, B, ldb, sb, beta, C,
+                ldc, c_type, epilogue, bias) -> int:
+    """Raw 8-bit integer product: returns the status code (no exception)."""
+    return _lib.gemm_run_i8(handle, kernel, stream, M, N, K, transB, alpha, A, lda, sa, B, ldb, sb,
+                            beta, C, ldc, c_type, epilogue, bias)
+
+
+def gemm_run_grouped_i8(handle, kernel, stream, groups, offsets, M, N, K, transB, alpha, A, lda, sa,
+                        B, ldb, stride_b, sb, beta, C, ldc, c_type, epilogue, bias) -> int:
+    """Raw grouped 8-bit integer product: returns the status code (no exception)."""
+    return _lib.gemm_run_grouped_i8(handle, kernel, stream, groups, offsets, M, N, K, transB, alpha,
+                                    A, lda, sa, B, ldb, stride_b, sb, beta, C, ldc, c_type, epilogue,
+                                    bias)
+
+
+def gemm_quantize_rows(handle, stream, M, K, X, ldx, x_type, Q, ldq, scales) -> int:
+    """Raw row quantization: returns the status code (no exception)."""
+    return _lib.gemm_quantize_rows(handle, stream, M, K, X, ldx, x_type, Q, ldq, scales)
+
+
+def gemm_check_args_grouped(groups, offsets, M, N, K, transB, A, lda, sa, B, ldb, stride_b, sb, C,
+                            ldc, i8, dtype, c_type, epilogue, bias) -> int:
+    """Pointers are integers (device addresses) or None.  Returns the status code."""
+    return _lib.gemm_check_args_grouped(groups, offsets, M, N, K, transB, A, lda, sa, B, ldb,
+                                        stride_b, sb, C, ldc, i8, dtype, c_type, epilogue, bias)
+
+
+def gemm_check_args_grouped_wgrad(groups, offsets, M, N, K, transB, A, lda, D, ldd, C, ldc,
+                                  stride_c, dtype, c_type, dbias) -> int:
+    return _lib.gemm_check_args_grouped_wgrad(groups, offsets, M, N, K, transB, A, lda, D, ldd, C,
+                                              ldc, stride_c, dtype, c_type, dbias)
+
+
+def gemm_check_args_quantize_rows(M, K, X, ldx, x_type, Q, ldq, scales) -> int:
+    return _lib.gemm_check_args_quantize_rows(M, K, X, ldx, x_type, Q, ldq, scales)
+
+
 # ----------------------------------------------------------------- tensor helpers --
 
 def _stream(stream):
@@ -421,6 +506,78 @@ def select_kernel_q(handle, M, N, K, *, bits, group, x_type="bf16", X=None, Wq=N
     return KERNEL_NAME[k]
 
 
+def run_grouped(handle, A, B, C, offsets, *, groups, M, N, K, trans_b=False, a_type="bf16",
+                alpha=1.0, beta=0.0, epilogue=GEMM_EPI_NONE, bias=None, lda=None, ldb=None,
+                stride_b=None, ldc=None, kernel=GEMM_GROUPED_AUTO, stream=None):
+    """C[r] = epi(alpha A[r] op(B_g) + beta C[r] + bias_g) for the rows r of each group g, on device
+    tensors: offsets holds groups + 1 int64 row numbers, B the groups' matrices one after another
+    (stride_b elements apart), bias fp32 groups x N.  Raises GemmError on a negative status."""
+    ldb = ldb if ldb is not None else (K if trans_b else N)
+    st = gemm_run_grouped(handle, int(kernel), _stream(stream), groups, _ptr(offsets), M, N, K,
+                          int(trans_b), float(alpha), _ptr(A), lda if lda is not None else K,
+                          _ptr(B), ldb,
+                          stride_b if stride_b is not None else (N if trans_b else K) * ldb,
+                          float(beta), _ptr(C), ldc if ldc is not None else N, DTYPE[a_type],
+                          int(epilogue), _ptr(bias))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_run_grouped")
+
+
+def run_grouped_wgrad(handle, A, D, C, offsets, *, groups, M, N, K, trans_b=False, a_type="bf16",
+                      c_type=None, alpha=1.0, beta=0.0, dbias=None, lda=None, ldd=None, ldc=None,
+                      stride_c=None, kernel=GEMM_GROUPED_AUTO, stream=None):
+    """C_g = alpha A_g^T D_g + beta C_g (K x N; with trans_b N x K) and, with dbias (fp32 groups x
+    N), the sums of D's rows by group: the gradients of run_grouped's B and bias.  Raises GemmError
+    on a negative status."""
+    ldc = ldc if ldc is not None else (K if trans_b else N)
+    st = gemm_run_grouped_wgrad(handle, int(kernel), _stream(stream), groups, _ptr(offsets), M, N, K,
+                                int(trans_b), float(alpha), _ptr(A), lda if lda is not None else K,
+                                _ptr(D), ldd if ldd is not None else N, float(beta), _ptr(C), ldc,
+                                stride_c if stride_c is not None else (N if trans_b else K) * ldc,
+                                DTYPE[a_type], DTYPE[c_type or a_type], _ptr(dbias))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_run_grouped_wgrad")
+
+
+def run_i8(handle, A, sa, B, sb, C, *, M, N, K, trans_b=False, c_type="bf16", alpha=1.0, beta=0.0,
+           epilogue=GEMM_EPI_NONE, bias=None, lda=None, ldb=None, ldc=None,
+           kernel=GEMM_GROUPED_AUTO, stream=None):
+    """C = epi(alpha sa[i] sb[j] (A op(B))[i][j] + beta C + bias) with 8-bit integers A and B, on
+    device tensors (sa fp32 M, sb fp32 N).  Raises GemmError on a negative status."""
+    st = gemm_run_i8(handle, int(kernel), _stream(stream), M, N, K, int(trans_b), float(alpha),
+                     _ptr(A), lda if lda is not None else K, _ptr(sa), _ptr(B),
+                     ldb if ldb is not None else (K if trans_b else N), _ptr(sb), float(beta),
+                     _ptr(C), ldc if ldc is not None else N, DTYPE[c_type], int(epilogue),
+                     _ptr(bias))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_run_i8")
+
+
+def run_grouped_i8(handle, A, sa, B, sb, C, offsets, *, groups, M, N, K, trans_b=False,
+                   c_type="bf16", alpha=1.0, beta=0.0, epilogue=GEMM_EPI_NONE, bias=None, lda=None,
+                   ldb=None, stride_b=None, ldc=None, kernel=GEMM_GROUPED_AUTO, stream=None):
+    """run_i8 by group, as run_grouped (sa fp32 M, sb and bias fp32 groups x N).  Raises GemmError
+    on a negative status."""
+    ldb = ldb if ldb is not None else (K if trans_b else N)
+    st = gemm_run_grouped_i8(handle, int(kernel), _stream(stream), groups, _ptr(offsets), M, N, K,
+                             int(trans_b), float(alpha), _ptr(A), lda if lda is not None else K,
+                             _ptr(sa), _ptr(B), ldb,
+                             stride_b if stride_b is not None else (N if trans_b else K) * ldb,
+                             _ptr(sb), float(beta), _ptr(C), ldc if ldc is not None else N,
+                             DTYPE[c_type], int(epilogue), _ptr(bias))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_run_grouped_i8")
+
+
+def quantize_rows(handle, X, Q, scales, *, M, K, x_type="bf16", ldx=None, ldq=None, stream=None):
+    """Q[i][k] = X[i][k] / scales[i] to the nearest 8-bit integer, scales[i] = max |X[i]| / 127.
+    Raises GemmError on a negative status."""
+    st = gemm_quantize_rows(handle, _stream(stream), M, K, _ptr(X), ldx if ldx is not None else K,
+                            DTYPE[x_type], _ptr(Q), ldq if ldq is not None else K, _ptr(scales))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_quantize_rows")
+
+
 class Gemm:
     """Owns one handle (gemm_create / gemm_destroy)."""
 
@@ -458,3 +615,18 @@ class Gemm:
 
     def select_kernel_q(self, M, N, K, **kw) -> str:
         return select_kernel_q(self.handle, M, N, K, **kw)
+
+    def run_grouped(self, A, B, C, offsets, **kw):
+        run_grouped(self.handle, A, B, C, offsets, **kw)
+
+    def run_grouped_wgrad(self, A, D, C, offsets, **kw):
+        run_grouped_wgrad(self.handle, A, D, C, offsets, **kw)
+
+    def run_i8(self, A, sa, B, sb, C, **kw):
+        run_i8(self.handle, A, sa, B, sb, C, **kw)
+
+    def run_grouped_i8(self, A, sa, B, sb, C, offsets, **kw):
+        run_grouped_i8(self.handle, A, sa, B, sb, C, offsets, **kw)
+
+    def quantize_rows(self, X, Q, scales, **kw):
+        quantize_rows(self.handle, X, Q, scales, **kw)

@@ -8,7 +8,7 @@ namespace tgemm {
 
 // E2M1 is OCP fp4: two elements per byte along the storage row, the even element in the
 // low nibble.
-enum DType : int { F32 = 0, F16 = 1, BF16 = 2, E4M3 = 3, E5M2 = 4, E2M1 = 5, E2M3 = 6, E3M2 = 7 };
+enum DType : int { F32 = 0, F16 = 1, BF16 = 2, E4M3 = 3, E5M2 = 4, E2M1 = 5, E2M3 = 6, E3M2 = 7, I8 = 8 };
 enum : uint32_t { EPI_BIAS = 1u, EPI_GELU = 2u };
 
 // Arguments every GEMM kernel receives (by value, in the kernel-argument segment).
@@ -44,6 +44,9 @@ struct GemmParams {
   uint8_t* sk_ws;
   int64_t sk_cnt_off;
   int sk_grid;
+  // 8-bit integers: the scale of row i of A and of column j of B (fp32).  Null otherwise.
+  const float* ra;
+  const float* rb;
 };
 
 // Workspace slot of one 256 x 128 output tile of the K loop split across two workgroups: its
@@ -60,6 +63,7 @@ template <int DT> struct DTypeInfo;
 template <> struct DTypeInfo<F32> { static constexpr int bytes = 4; };
 template <> struct DTypeInfo<F16> { static constexpr int bytes = 2; };
 template <> struct DTypeInfo<BF16> { static constexpr int bytes = 2; };
+template <> struct DTypeInfo<I8> { static constexpr int bytes = 1; };
 template <> struct DTypeInfo<E4M3> { static constexpr int bytes = 1; };
 template <> struct DTypeInfo<E5M2> { static constexpr int bytes = 1; };
 // The matrix-core kernels see packed fp4 rows as bytes (two elements each), and packed 6-bit
