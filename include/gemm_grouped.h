@@ -26,8 +26,17 @@ extern "C" {
 /* Kernels of the entry points below.  AUTO picks by type, layout, alignment and size. */
 typedef enum gemm_grouped_kernel {
   GEMM_GROUPED_AUTO = 0,
-  GEMM_GROUPED_ANY = 1, /* matrix cores fed element by element through LDS, 64x64 tile: any
-                           alignment, layout and size */
+  GEMM_GROUPED_ANY = 1, /* 64x64 tile, copies through registers: any alignment, layout and size */
+  /* The tiles below copy 16-byte chunks: A, B (D) and C start on 16 bytes, the rows of A and B (D)
+     and B's matrices follow each other at whole multiples of 16 bytes (at most 2^23 a row), the
+     rows and matrices of C at multiples of 4 elements. */
+  GEMM_GROUPED_MFMA_64 = 2,      /* 64x64 tile, the K loop split between two groups of waves */
+  GEMM_GROUPED_MFMA_128 = 3,     /* 128x128 tile, likewise */
+  GEMM_GROUPED_MFMA_256x128 = 4, /* 256x128 tile */
+  GEMM_GROUPED_MFMA_256 = 5,     /* 256x256 tile */
+  GEMM_GROUPED_STREAM = 6,       /* few rows a group (decoding): weights streamed through registers,
+                                    16 to 64 rows a tile, any alignment; rows of A and B of at most
+                                    2^23 bytes, N >= 4 for a B stored K x N; not the gradient */
 } gemm_grouped_kernel_t;
 
 /* The product of each group's rows with the group's own matrix:

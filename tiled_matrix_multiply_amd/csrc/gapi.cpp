@@ -9,12 +9,19 @@
 #include "handle.hpp"
 
 namespace tgemm {
-hipError_t launch_grouped_any(const GemmParams& p, const GroupArgs& ga, int type, int c_type, bool b_mn,
-                              hipStream_t s);
-hipError_t launch_grouped_wgrad_any(const GemmParams& p, const GroupArgs& ga, int type, int c_type,
-                                    hipStream_t s);
-hipError_t launch_bias_grad(const void* D, int64_t ldd, int M, int N, int type, const GroupArgs& ga,
-                            float* dbias, hipStream_t s);
+// grouped_mfma.hpp's tiles (its GroupedTile numbers; 0: any alignment)
+hipError_t launch_grouped_f16(const GemmParams&, const GroupArgs&, bool b_mn, int tile, int cus, hipStream_t);
+hipError_t launch_grouped_bf16(const GemmParams&, const GroupArgs&, bool b_mn, int tile, int cus, hipStream_t);
+hipError_t launch_grouped_i8_f16(const GemmParams&, const GroupArgs&, bool b_mn, int tile, int cus, hipStream_t);
+hipError_t launch_grouped_i8_bf16(const GemmParams&, const GroupArgs&, bool b_mn, int tile, int cus, hipStream_t);
+hipError_t launch_grouped_i8_f32(const GemmParams&, const GroupArgs&, bool b_mn, int tile, int cus, hipStream_t);
+hipError_t launch_grouped_wgrad_f16(const GemmParams&, const GroupArgs&, const BiasGrad&, int c_type, int tile,
+                                    hipStream_t);
+hipError_t launch_grouped_wgrad_bf16(const GemmParams&, const GroupArgs&, const BiasGrad&, int c_type, int tile,
+                                     hipStream_t);
+hipError_t launch_stream_f16(const GemmParams&, const GroupArgs&, int c_type, bool kn, int rows, int waves, hipStream_t);
+hipError_t launch_stream_bf16(const GemmParams&, const GroupArgs&, int c_type, bool kn, int rows, int waves, hipStream_t);
+hipError_t launch_stream_i8(const GemmParams&, const GroupArgs&, int c_type, bool kn, int rows, int waves, hipStream_t);
 hipError_t launch_quantize_rows(const void* X, int64_t ldx, int M, int K, int x_type, int8_t* Q, int64_t ldq,
                                 float* scales, hipStream_t s);
 }  // namespace tgemm
@@ -135,34 +142,120 @@ bool valid(gemm_handle_t h) { return h && h->magic == tgemm::kHandleMagic; }
 
 gemm_status_t status(hipError_t e) { return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH; }
 
-// Tiles of 64 x 64, the smallest, must be countable in 31 bits.
-bool countable(int64_t row_tiles, int64_t n) { return (__int128)row_tiles * ((n + 63) / 64) <= kMaxDim; }
+constexpr int64_t kMaxRowBytes = int64_t(1) << 23;  // the kernels' 32-bit lane offsets span up to 256 rows
+
+// The tiled kernels read 16-byte chunks of both operands and store runs of C.
+bool tiles_fit(const GArgs& a) {
+  const int in = a.i8 ? 1 : es(a.at);
+  auto rows_ok = [&](const void* p, int64_t ld) {
+    return aligned(p, 16) && ld * in % 16 == 0 && ld * in <= kMaxRowBytes;
+  };
+  const bool reads = a.wgrad ? a.M > 0 : a.K > 0;
+  if (reads && (!rows_ok(a.A, a.lda) || !rows_ok(a.B, a.ldb) || a.stride_b * in % 16 != 0)) return false;
+  return aligned(a.C, 16) && a.ldc % 4 == 0 && a.stride_c % 4 == 0;
+}
+// The streaming kernel takes any alignment; stored K x N, four columns at a time.
+bool stream_fits(const GArgs& a) {
+  const int in = a.i8 ? 1 : es(a.at);
+  return !a.wgrad && (a.transB || a.N >= 4) && a.lda * in <= kMaxRowBytes && a.ldb * in <= kMaxRowBytes;
+}
+
+// Groups that can hold rows, and the rows of one on average.
+int64_t live_groups(const GArgs& a) { return a.groups < a.M ? a.groups : a.M; }
+
+// Row tiles of height bm to expect: every group's last one is half empty on average (a single
+// group's number is known).
+int64_t expected_tiles(const GArgs& a, int64_t bm, int64_t bn) {
+  const int64_t rows = a.groups == 1 ? (a.M + bm - 1) / bm : (a.M + live_groups(a) * (bm / 2) + bm - 1) / bm;
+  return rows * ((a.N + bn - 1) / bn);
+}
+
+gemm_grouped_kernel_t pick(const GArgs& a, int cus) {
+  if (a.wgrad) {
+    if (!tiles_fit(a)) return GEMM_GROUPED_ANY;
+    auto tiles = [&](int64_t bm, int64_t bn) { return (a.N + bm - 1) / bm * ((a.K + bn - 1) / bn) * a.groups; };
+    if (tiles(256, 256) >= cus) return GEMM_GROUPED_MFMA_256;
+    if (tiles(128, 128) >= cus / 2) return GEMM_GROUPED_MFMA_128;
+    return GEMM_GROUPED_MFMA_64;
+  }
+  const int64_t rows = (a.M + live_groups(a) - 1) / live_groups(a);
+  if (rows <= 64 && stream_fits(a)) return GEMM_GROUPED_STREAM;
+  if (!tiles_fit(a)) return GEMM_GROUPED_ANY;
+  if (expected_tiles(a, 256, 256) >= cus) return GEMM_GROUPED_MFMA_256;
+  if (expected_tiles(a, 128, 128) > cus && expected_tiles(a, 256, 128) <= cus) return GEMM_GROUPED_MFMA_256x128;
+  if (16 * expected_tiles(a, 128, 128) >= 9 * cus) return GEMM_GROUPED_MFMA_128;
+  return GEMM_GROUPED_MFMA_64;
+}
+
+int tile_of(gemm_grouped_kernel_t k) {  // GroupedTile
+  switch (k) {
+    case GEMM_GROUPED_MFMA_64: return 1;
+    case GEMM_GROUPED_MFMA_128: return 2;
+    case GEMM_GROUPED_MFMA_256x128: return 3;
+    case GEMM_GROUPED_MFMA_256: return 4;
+    default: return 0;
+  }
+}
+
+// The kernel of a call, or an error: kernels asked for by name have to fit.
+gemm_status_t choose(const GArgs& a, int cus, gemm_grouped_kernel_t& k) {
+  switch (k) {
+    case GEMM_GROUPED_AUTO: k = pick(a, cus); return GEMM_OK;
+    case GEMM_GROUPED_ANY: return GEMM_OK;
+    case GEMM_GROUPED_STREAM: return stream_fits(a) ? GEMM_OK : GEMM_ERR_UNSUPPORTED;
+    case GEMM_GROUPED_MFMA_64:
+    case GEMM_GROUPED_MFMA_128:
+    case GEMM_GROUPED_MFMA_256x128:
+    case GEMM_GROUPED_MFMA_256: return tiles_fit(a) ? GEMM_OK : GEMM_ERR_UNSUPPORTED;
+    default: return GEMM_ERR_INVALID_VALUE;
+  }
+}
+
+// Tiles must be countable in 31 bits, with the worst case's row tiles and a last round of 8.
+bool countable(int64_t row_tiles, int64_t n, int64_t bn) {
+  return (__int128)row_tiles * ((n + bn - 1) / bn) <= kMaxDim - 16;
+}
 
 gemm_status_t run_rows(gemm_handle_t h, gemm_grouped_kernel_t kernel, void* stream, const GArgs& a, float alpha,
                        float beta, void* C) {
   if (!valid(h)) return GEMM_ERR_INVALID_HANDLE;
-  const gemm_status_t st = check(a);
+  gemm_status_t st = check(a);
   if (st != GEMM_OK) return st;
   if (a.M == 0 || a.N == 0 || a.groups == 0) return GEMM_OK;
-  if (!countable(tgemm::max_row_tiles(a.M, a.groups, 64), a.N)) return GEMM_ERR_UNSUPPORTED;
-  if (kernel != GEMM_GROUPED_AUTO && kernel != GEMM_GROUPED_ANY) return GEMM_ERR_INVALID_VALUE;
+  if (!countable(tgemm::max_row_tiles(a.M, a.groups, 64), a.N, 64)) return GEMM_ERR_UNSUPPORTED;
+  if ((st = choose(a, h->cu_count, kernel)) != GEMM_OK) return st;
   tgemm::GemmParams p = params(a, alpha, beta, C);
   p.bias = (a.epi & GEMM_EPI_BIAS) ? a.bias : nullptr;
   p.ra = a.sa;
   p.rb = a.sb;
   const tgemm::GroupArgs ga{a.offsets, (int)a.groups, a.stride_b, 0};
-  const int type = a.i8 ? tgemm::I8 : (int)a.at;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool kn = a.transB == 0;
   tgemm::DeviceGuard g(h->device);
-  return status(tgemm::launch_grouped_any(p, ga, type, a.ct, a.transB == 0, static_cast<hipStream_t>(stream)));
+  if (kernel == GEMM_GROUPED_STREAM) {
+    const int64_t avg = (a.M + live_groups(a) - 1) / live_groups(a);
+    const int rows = avg <= (a.groups == 1 ? 16 : 10) ? 16 : avg <= (a.groups == 1 ? 32 : 24) ? 32 : 64;
+    if (!countable(tgemm::max_row_tiles(a.M, a.groups, rows), a.N, kn ? 64 : 32)) return GEMM_ERR_UNSUPPORTED;
+    const int waves = rows == 64 && kn ? 4 : 8;
+    return status(a.i8              ? tgemm::launch_stream_i8(p, ga, a.ct, kn, rows, waves, s)
+                  : a.at == GEMM_F16 ? tgemm::launch_stream_f16(p, ga, a.ct, kn, rows, waves, s)
+                                     : tgemm::launch_stream_bf16(p, ga, a.ct, kn, rows, waves, s));
+  }
+  const int tile = tile_of(kernel);
+  if (!a.i8) return status(a.at == GEMM_F16 ? tgemm::launch_grouped_f16(p, ga, kn, tile, h->cu_count, s) : tgemm::launch_grouped_bf16(p, ga, kn, tile, h->cu_count, s));
+  return status(a.ct == GEMM_F32   ? tgemm::launch_grouped_i8_f32(p, ga, kn, tile, h->cu_count, s)
+                : a.ct == GEMM_F16 ? tgemm::launch_grouped_i8_f16(p, ga, kn, tile, h->cu_count, s)
+                                   : tgemm::launch_grouped_i8_bf16(p, ga, kn, tile, h->cu_count, s));
 }
 
 gemm_status_t run_wgrad(gemm_handle_t h, gemm_grouped_kernel_t kernel, void* stream, const GArgs& a, float alpha,
                         float beta, void* C, float* dbias) {
   if (!valid(h)) return GEMM_ERR_INVALID_HANDLE;
-  const gemm_status_t st = check(a);
+  gemm_status_t st = check(a);
   if (st != GEMM_OK) return st;
   if (a.N == 0 || a.groups == 0 || (a.K == 0 && !dbias)) return GEMM_OK;
-  if (kernel != GEMM_GROUPED_AUTO && kernel != GEMM_GROUPED_ANY) return GEMM_ERR_INVALID_VALUE;
+  if (kernel == GEMM_GROUPED_STREAM) return GEMM_ERR_UNSUPPORTED;
+  if ((st = choose(a, h->cu_count, kernel)) != GEMM_OK) return st;
   const tgemm::GroupArgs ga{a.offsets, (int)a.groups, 0, a.stride_c};
   // The kernels compute C = X^T Y: stored N x K, the gradient is D^T A.
   tgemm::GemmParams p = params(a, alpha, beta, C);
@@ -174,15 +267,13 @@ gemm_status_t run_wgrad(gemm_handle_t h, gemm_grouped_kernel_t kernel, void* str
   p.N = (int)(a.transB ? a.K : a.N);
   p.K = (int)a.M;
   p.epi = 0;
-  if (!countable(((int64_t)p.M + 63) / 64 * a.groups, p.N)) return GEMM_ERR_UNSUPPORTED;
+  const int64_t tiles = ((int64_t)p.M + 63) / 64 * (((int64_t)p.N + 63) / 64 + 7);
+  if (!countable(((a.N + 63) / 64 + tiles) * a.groups, 1, 1)) return GEMM_ERR_UNSUPPORTED;
+  const tgemm::BiasGrad b{a.B, a.ldb, (int)a.N, 0, 0, dbias};
   const hipStream_t s = static_cast<hipStream_t>(stream);
   tgemm::DeviceGuard g(h->device);
-  if (dbias) {
-    const hipError_t e = tgemm::launch_bias_grad(a.B, a.ldb, (int)a.M, (int)a.N, a.at, ga, dbias, s);
-    if (e != hipSuccess) return GEMM_ERR_LAUNCH;
-  }
-  if (a.K == 0) return GEMM_OK;
-  return status(tgemm::launch_grouped_wgrad_any(p, ga, a.at, a.ct, s));
+  return status(a.at == GEMM_F16 ? tgemm::launch_grouped_wgrad_f16(p, ga, b, a.ct, tile_of(kernel), s)
+                                 : tgemm::launch_grouped_wgrad_bf16(p, ga, b, a.ct, tile_of(kernel), s));
 }
 
 gemm_status_t check_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, gemm_dtype_t xt, const void* Q,

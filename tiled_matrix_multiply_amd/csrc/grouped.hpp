@@ -23,6 +23,21 @@ inline int64_t max_row_tiles(int64_t M, int64_t groups, int64_t bm) {
   return (M + live * (bm - 1)) / bm;
 }
 
+// Scans across the wave, lane by lane upwards (six vector instructions each, no LDS): the running
+// maximum and the running sum of non-negative values.
+template <class F>
+__device__ __forceinline__ int scan_up(int v, F f) {
+  v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));  // row_shr 1, 2, 4, 8
+  v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+  v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+  v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+  v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));  // row_bcast 15
+  v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));  // row_bcast 31
+  return v;
+}
+__device__ __forceinline__ int scan_max(int v) { return scan_up(v, [](int a, int b) { return max(a, b); }); }
+__device__ __forceinline__ int scan_add(int v) { return scan_up(v, [](int a, int b) { return a + b; }); }
+
 // 64 consecutive groups, one per lane: group base + lane owns rows [row0, row0 + rows).
 // Offsets are clamped to 0 .. M and raised to the largest before them (`carry`), so groups never
 // overlap and never leave the matrix whatever the array holds.
@@ -36,67 +51,104 @@ __device__ __forceinline__ GroupLane group_lane(const GroupArgs& ga, int M, int 
                                                 int& carry) {
   const int g = base + lane;
   int hi = g < ga.groups ? clamp_offset(ga.offsets[g + 1], M) : 0;
-  hi = max(hi, carry);
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(hi, d);
-    if (lane >= d) hi = max(hi, o);
-  }
-  int lo = __shfl_up(hi, 1);
-  if (lane == 0) lo = carry;
-  carry = __shfl(hi, 63);
+  hi = scan_max(max(hi, carry));
+  const int lo = __builtin_amdgcn_update_dpp(carry, hi, 0x138, 0xf, 0xf, false);  // wave_shr 1
+  carry = __builtin_amdgcn_readlane(hi, 63);
   return GroupLane{lo, hi - lo};
 }
 
-// Rows of one group (wave-uniform).
-__device__ __forceinline__ GroupLane group_rows(const GroupArgs& ga, int M, int g, int lane) {
-  if (!ga.offsets) return GroupLane{0, M};
-  int carry = clamp_offset(ga.offsets[0], M);
-  GroupLane r{};
-  for (int base = 0; base <= g; base += 64) r = group_lane(ga, M, base, lane, carry);
-  return GroupLane{__builtin_amdgcn_readlane(r.row0, g & 63), __builtin_amdgcn_readlane(r.rows, g & 63)};
+// Workgroups are dealt to the 8 XCDs round-robin by id: workgroup bid takes item number bid / 8 of
+// XCD bid % 8, each XCD a contiguous range of the items that there really are, so that the items
+// on one XCD share rows and weights in that XCD's L2.  The grid holds whole rounds of 8.  -1: none.
+__device__ __forceinline__ int xcd_item(int bid, int items) {
+  const int x = bid & 7, i = bid >> 3, q = items >> 3, r = items & 7;
+  return i < q + (x < r) ? x * q + min(x, r) + i : -1;
 }
 
-// Work item t of the sequence that lists, group after group, ceil(rows / bm) * per_row items.
+// An item of the sequence that lists, group after group, own(rows) * per items.
 struct GroupItem {
-  int group;  // -1: t is past the last item
-  int row0, rows;
+  int group, row0, rows;
   int local;  // index within the group
 };
-__device__ __forceinline__ int scan_add(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
-  return v;
-}
-__device__ __forceinline__ int group_items(const GroupArgs& ga, int M, int bm, int per_row, int lane) {
-  if (!ga.offsets) return (M + bm - 1) / bm * per_row;
-  int carry = clamp_offset(ga.offsets[0], M), total = 0;
-  for (int base = 0; base < ga.groups; base += 64) {
-    const GroupLane r = group_lane(ga, M, base, lane, carry);
-    total += __shfl(scan_add((r.rows + bm - 1) / bm, lane), 63);
-  }
-  return __builtin_amdgcn_readfirstlane(total) * per_row;
-}
-__device__ __forceinline__ GroupItem group_item(const GroupArgs& ga, int M, int bm, int per_row, int t,
-                                                int lane) {
-  if (!ga.offsets) return GroupItem{t < (M + bm - 1) / bm * per_row ? 0 : -1, 0, M, t};
-  int carry = clamp_offset(ga.offsets[0], M), before = 0;
-  for (int base = 0; base < ga.groups; base += 64) {
-    const GroupLane r = group_lane(ga, M, base, lane, carry);
-    const int own = (r.rows + bm - 1) / bm, end = before + scan_add(own, lane);
-    const uint64_t hit = __ballot((int64_t)end * per_row > t);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      return GroupItem{base + l, __builtin_amdgcn_readlane(r.row0, l), __builtin_amdgcn_readlane(r.rows, l),
-                       t - __builtin_amdgcn_readlane(end - own, l) * per_row};
+
+// The groups as one wave sees them (every lane active): up to 64 of them are held in registers,
+// more are walked again for each question.
+struct Groups {
+  const GroupArgs& ga;
+  int M, lane, first;
+  GroupLane r;
+  __device__ __forceinline__ Groups(const GroupArgs& a, int M_, int lane_) : ga(a), M(M_), lane(lane_), first(0) {
+    if (!ga.offsets) {
+      r = GroupLane{lane ? M : 0, lane ? 0 : M};
+      return;
     }
-    before = __shfl(end, 63);
+    first = clamp_offset(ga.offsets[0], M);
+    int carry = first;
+    r = group_lane(ga, M, 0, lane, carry);
   }
-  return GroupItem{-1, 0, 0, 0};
+  __device__ __forceinline__ bool held() const { return ga.groups <= 64; }
+  template <class F>
+  __device__ __forceinline__ int total(F own) const {
+    if (held()) return __builtin_amdgcn_readlane(scan_add(own(r.rows)), 63);
+    int carry = first, sum = 0;
+    for (int base = 0; base < ga.groups; base += 64)
+      sum += __builtin_amdgcn_readlane(scan_add(own(group_lane(ga, M, base, lane, carry).rows)), 63);
+    return sum;
+  }
+  // Item t, which is below total(own) * per.
+  template <class F>
+  __device__ __forceinline__ GroupItem find(F own, int per, int t) const {
+    GroupLane q = r;
+    int n = own(q.rows), end = scan_add(n), base = 0;
+    if (!held()) {
+      int carry = first, before = 0;
+      for (;; base += 64) {
+        q = group_lane(ga, M, base, lane, carry);
+        n = own(q.rows);
+        end = before + scan_add(n);
+        before = __builtin_amdgcn_readlane(end, 63);
+        if (before * per > t || base + 64 >= ga.groups) break;
+      }
+    }
+    const int l = __builtin_ctzll(__ballot(end * per > t) | (1ull << 63));
+    return GroupItem{base + l, __builtin_amdgcn_readlane(q.row0, l), __builtin_amdgcn_readlane(q.rows, l),
+                     t - __builtin_amdgcn_readlane(end - n, l) * per};
+  }
+  __device__ __forceinline__ GroupLane rows_of(int g) const {
+    GroupLane q = r;
+    if (!held()) {
+      int carry = first;
+      for (int base = 0; base <= g; base += 64) q = group_lane(ga, M, base, lane, carry);
+    }
+    return GroupLane{__builtin_amdgcn_readlane(q.row0, g & 63), __builtin_amdgcn_readlane(q.rows, g & 63)};
+  }
+  // The j-th group in falling order of the power of two below its rows (up to 64 groups; more keep
+  // their own order): work whose time goes with the rows is best begun with the longest.
+  __device__ __forceinline__ int by_size(int j) const {
+    if (!held()) return j;
+    const int size = lane < ga.groups ? 32 - __clz(r.rows) : -1;
+    for (int c = 32 - __clz(M); c >= 0; --c) {
+      const uint64_t m = __ballot(size == c);
+      const int n = __popcll(m);
+      if (j < n) {
+        const int rank = __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+        return __builtin_ctzll(__ballot(size == c && rank == j) | (1ull << 63));
+      }
+      j -= n;
+    }
+    return j;  // past the last group
+  }
+};
+
+// Item `bid` of the sequence with ceil(rows / bm) * per items a group, dealt out by xcd_item; group
+// -1: none (the grid is sized for the worst case).
+__device__ __forceinline__ GroupItem group_item(const GroupArgs& ga, int M, int bm, int per, int bid, int lane) {
+  const Groups gs(ga, M, lane);
+  auto own = [bm](int rows) { return (rows + bm - 1) / bm; };
+  const int t = xcd_item(bid, gs.total(own) * per);
+  return t < 0 ? GroupItem{-1, 0, 0, 0} : gs.find(own, per, t);
 }
+inline int64_t whole_rounds(int64_t items) { return (items + 7) / 8 * 8; }
 
 // Moves the arguments of a product on to one group: its rows of A and C (and their scales), its
 // B, bias and column scales.
@@ -120,5 +172,17 @@ __device__ __forceinline__ void enter_group_wgrad(GemmParams& p, const GroupArgs
   p.C = reinterpret_cast<uint8_t*>(p.C) + (int64_t)group * ga.stride_c * CES;
   p.K = rows;
 }
+
+// The bias gradient, dbias_g[n] = the sum of D's rows of group g, is the work of the first
+// workgroups of the weight gradient's grid (64 columns of one group each), so that it runs beside
+// the products and costs no launch.  Lane l sums 8 columns of every (threads / 8)-th row; the
+// lanes of a wave meet by shuffles and the waves in LDS, in an order that depends on the group's
+// size alone.
+struct BiasGrad {
+  const void* D;
+  int64_t ldd;
+  int N, blocks_n, blocks;  // blocks: all of them, a whole number of rounds of 8 (0: none)
+  float* out;
+};
 
 }  // namespace tgemm

@@ -1,0 +1,291 @@
+// Grouped and 8-bit integer products for few rows per group (gfx950 only): decoding, where the
+// weights are read once and nothing else matters.
+//
+// A workgroup owns a block of columns of one group and up to 16 MF of its rows; its waves share
+// out K and meet in LDS at the end, in wave order.  Weights and rows go straight from global
+// memory into the registers of 16 x 16 matrix instructions: nothing in the loop waits on another
+// wave, and each wave keeps two sets of U steps (64 bytes of K) in flight.
+//  * B stored N x K: a lane loads 16 bytes of K of its column, NF = 2 fragments of 16 columns.
+//  * B stored K x N: a lane loads its 4 columns from each of the rows of K that its 16 bytes of a
+//    fragment stand for and transposes them with byte permutes: 64 columns, NF = 4 fragments
+//    (column 4 i + j of the block is row i of fragment j).
+// Any alignment and size: loads are unaligned, columns past N repeat the last ones and are not
+// stored, and the last, partial step of K is loaded element by element.
+#pragma once
+
+#include <type_traits>
+
+#include "grouped.hpp"
+
+namespace tgemm {
+
+typedef int s_i32x4 __attribute__((ext_vector_type(4)));
+typedef float s_f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 s_bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 s_f16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t s_u32x4 __attribute__((ext_vector_type(4)));
+
+template <int DT, class Acc>
+__device__ __forceinline__ Acc mma16(s_u32x4 x, s_u32x4 y, Acc c) {
+  if constexpr (DT == I8)
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(s_i32x4, x), __builtin_bit_cast(s_i32x4, y), c, 0, 0, 0);
+  else if constexpr (DT == BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(s_bf16x8, x), __builtin_bit_cast(s_bf16x8, y), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(s_f16x8, x), __builtin_bit_cast(s_f16x8, y), c, 0, 0, 0);
+}
+
+template <int DT, bool KN, int MF>
+struct StreamCfg {
+  static constexpr int ES = DTypeInfo<DT>::bytes, CE = 16 / ES;  // elements of a lane's 16 bytes
+  static constexpr int KS = 64 / ES;                             // K of a step
+  static constexpr int NF = KN ? 4 : 2, BN = 16 * NF, BM = 16 * MF;
+  static constexpr int U = MF == 4 ? 2 : KN ? 2 : 4;             // steps loaded together
+  static constexpr int CB = 4 * ES;                              // bytes of a K x N row a lane loads
+  static constexpr int BD = KN ? CE * CB / 4 : 4 * NF;           // dwords of B a lane loads a step
+  static constexpr int PART = NF * MF * 64 * 16;                 // bytes of one wave's sums
+};
+
+template <int DT, bool KN, int MF>
+__global__ __launch_bounds__(512) void stream_kernel(GemmParams p, GroupArgs ga, int c_type) {
+  using C = StreamCfg<DT, KN, MF>;
+  using Acc = typename std::conditional<DT == I8, s_i32x4, s_f32x4>::type;
+  constexpr int ES = C::ES, CE = C::CE, KS = C::KS, NF = C::NF, U = C::U;
+  extern __shared__ __attribute__((aligned(16))) uint8_t part[];
+  const int lane = threadIdx.x & 63, NW = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const GroupItem it = group_item(ga, p.M, C::BM, p.tiles_n, (int)blockIdx.x, lane);
+  if (it.group < 0) return;
+  {
+    const int ces = c_type == F32 ? 4 : 2;
+    if (ces == 4) enter_group<ES, 4>(p, ga, it.group, it.row0, it.rows);
+    else enter_group<ES, 2>(p, ga, it.group, it.row0, it.rows);
+  }
+  // the row tiles of a block of columns are neighbours: they share its weights in the L2
+  const int tiles_m = (p.M + C::BM - 1) / C::BM;
+  const int m0 = it.local % tiles_m * C::BM, n0 = it.local / tiles_m * C::BN;
+  const int q = lane >> 4, l16 = lane & 15;
+
+  const uint8_t* const A = reinterpret_cast<const uint8_t*>(p.A);
+  const uint8_t* const B = reinterpret_cast<const uint8_t*>(p.B);
+  // Lane offsets (32 bits: the host keeps a row under 2^23 bytes) from a uniform base.
+  uint32_t oa[MF], ob[KN ? 1 : NF];
+#pragma unroll
+  for (int f = 0; f < MF; ++f) oa[f] = (uint32_t)((16 * f + l16 < p.M - m0 ? 16 * f + l16 : p.M - 1 - m0) * (int)(p.lda * ES)) + 16 * q;
+  const uint8_t* const Ab = A + (int64_t)m0 * p.lda * ES;
+  const int nc = n0 + 4 * l16;                      // K x N: the lane's columns, from nl on
+  const int nl = KN ? min(nc, p.N - 4) : 0;
+  const uint8_t* const Bb = KN ? B : B + (int64_t)n0 * p.ldb * ES;
+  if constexpr (KN) {
+    ob[0] = (uint32_t)(q * CE) * (uint32_t)(p.ldb * ES) + (uint32_t)nl * ES;
+  } else {
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+      ob[f] = (uint32_t)min(16 * f + l16, p.N - 1 - n0) * (uint32_t)(p.ldb * ES) + 16 * q;
+  }
+
+  struct Step {
+    uint32_t b[C::BD];
+    s_u32x4 a[MF];
+  };
+  auto load = [&](int s, Step& t) {
+    const uint8_t* const as = Ab + (int64_t)s * 64;
+#pragma unroll
+    for (int f = 0; f < MF; ++f) __builtin_memcpy(&t.a[f], as + oa[f], 16);
+    if constexpr (KN) {
+      const int64_t row = p.ldb * ES;
+      const uint8_t* const bs = Bb + (int64_t)s * KS * row;
+#pragma unroll
+      for (int i = 0; i < CE; ++i) __builtin_memcpy(&t.b[i * (C::CB / 4)], bs + i * row + ob[0], C::CB);
+    } else {
+      const uint8_t* const bs = Bb + (int64_t)s * 64;
+#pragma unroll
+      for (int f = 0; f < NF; ++f) __builtin_memcpy(&t.b[4 * f], bs + ob[f], 16);
+    }
+  };
+  // The partial step after the last whole one: zeros past K on both sides.
+  auto load_tail = [&](int s, Step& t) {
+    const int64_t k = (int64_t)s * KS + q * CE;
+    const int n = (int)min((int64_t)CE, max((int64_t)0, p.K - k));  // elements of this lane
+    auto elems = [&](const uint8_t* src, int count, s_u32x4& v) {
+      v = s_u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < CE; ++e)
+        if (e < count) {
+          const uint32_t x = ES == 1 ? src[e] : reinterpret_cast<const uint16_t*>(src)[e];
+          v[e * ES / 4] |= x << (8 * (e * ES % 4));
+        }
+    };
+#pragma unroll
+    for (int f = 0; f < MF; ++f) elems(Ab + (int64_t)s * 64 + oa[f], n, t.a[f]);
+    if constexpr (KN) {
+      const int64_t row = p.ldb * ES;
+#pragma unroll
+      for (int i = 0; i < CE; ++i) {
+#pragma unroll
+        for (int d = 0; d < C::CB / 4; ++d) t.b[i * (C::CB / 4) + d] = 0u;
+        if (i < n) __builtin_memcpy(&t.b[i * (C::CB / 4)], Bb + ((int64_t)s * KS + i) * row + ob[0], C::CB);
+      }
+    } else {
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        s_u32x4 v;
+        elems(Bb + (int64_t)s * 64 + ob[f], n, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t.b[4 * f + e] = v[e];
+      }
+    }
+  };
+  // Fragment j of B from a step's registers.
+  auto frags = [&](const Step& t, s_u32x4 (&b)[NF]) {
+    if constexpr (!KN) {
+#pragma unroll
+      for (int f = 0; f < NF; ++f) b[f] = s_u32x4{t.b[4 * f], t.b[4 * f + 1], t.b[4 * f + 2], t.b[4 * f + 3]};
+    } else if constexpr (ES == 2) {
+      // row i of K holds columns 0, 1 in its first dword and 2, 3 in its second
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          b[j][d] = __builtin_amdgcn_perm(t.b[2 * (2 * d + 1) + j / 2], t.b[2 * (2 * d) + j / 2],
+                                          j & 1 ? 0x07060302u : 0x05040100u);
+    } else {
+      // 4 x 4 bytes: rows 4 d .. 4 d + 3 of K, columns 0 .. 3
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const uint32_t* r = &t.b[4 * d];
+        const uint32_t x0 = __builtin_amdgcn_perm(r[1], r[0], 0x05010400u), x1 = __builtin_amdgcn_perm(r[3], r[2], 0x05010400u);
+        const uint32_t y0 = __builtin_amdgcn_perm(r[1], r[0], 0x07030602u), y1 = __builtin_amdgcn_perm(r[3], r[2], 0x07030602u);
+        b[0][d] = __builtin_amdgcn_perm(x1, x0, 0x05040100u);
+        b[1][d] = __builtin_amdgcn_perm(x1, x0, 0x07060302u);
+        b[2][d] = __builtin_amdgcn_perm(y1, y0, 0x05040100u);
+        b[3][d] = __builtin_amdgcn_perm(y1, y0, 0x07060302u);
+      }
+    }
+  };
+  Acc acc[NF][MF];
+#pragma unroll
+  for (int j = 0; j < NF; ++j)
+#pragma unroll
+    for (int f = 0; f < MF; ++f) acc[j][f] = Acc{0, 0, 0, 0};
+  auto mul = [&](const Step& t) {
+    s_u32x4 b[NF];
+    frags(t, b);
+#pragma unroll
+    for (int j = 0; j < NF; ++j)
+#pragma unroll
+      for (int f = 0; f < MF; ++f) acc[j][f] = mma16<DT>(b[j], t.a[f], acc[j][f]);
+  };
+
+  // Whole steps in blocks of U, block after block over the waves; then the last few steps one by
+  // one, and the partial step.
+  const int steps = p.K / KS, blocks = steps / U;
+  Step x[U], y[U];
+  auto load_block = [&](int b, Step (&t)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(b * U + u, t[u]);
+  };
+  auto mul_block = [&](const Step (&t)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) mul(t[u]);
+  };
+  int b = wave;
+  if (b < blocks) load_block(b, x);
+  while (b < blocks) {
+    const int b1 = b + NW, b2 = b1 + NW;
+    if (b1 < blocks) load_block(b1, y);
+    mul_block(x);
+    if (b1 >= blocks) break;
+    if (b2 < blocks) load_block(b2, x);
+    mul_block(y);
+    b = b2;
+  }
+  for (int s = blocks * U + wave; s < steps; s += NW) {
+    load(s, x[0]);
+    mul(x[0]);
+  }
+  if (steps * KS < p.K && wave == (steps - blocks * U) % NW) {
+    load_tail(steps, x[0]);
+    mul(x[0]);
+  }
+
+  Acc* const mine = reinterpret_cast<Acc*>(part + wave * C::PART);
+#pragma unroll
+  for (int j = 0; j < NF; ++j)
+#pragma unroll
+    for (int f = 0; f < MF; ++f) mine[(j * MF + f) * 64 + lane] = acc[j][f];
+  __syncthreads();
+
+  // Item i of 16 MF rows x BN columns in runs of four columns.  A lane of fragment (j, f) holds row
+  // 16 f + l16 and, in register r, the fragment's row 4 q + r.
+  for (int i = threadIdx.x; i < NF * MF * 64; i += blockDim.x) {
+    int m, n;
+    Acc v = Acc{0, 0, 0, 0};
+    if constexpr (KN) {
+      const int r = i & 3, l = (i >> 2) & 63, f = i >> 8;
+      m = m0 + 16 * f + (l & 15);
+      n = n0 + 16 * (l >> 4) + 4 * r;
+      for (int w = 0; w < NW; ++w) {
+        const Acc* src = reinterpret_cast<const Acc*>(part + w * C::PART);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += src[(j * MF + f) * 64 + l][r];
+      }
+    } else {
+      const int l = i & 63, jf = i >> 6;
+      m = m0 + 16 * (jf % MF) + (l & 15);
+      n = n0 + 16 * (jf / MF) + 4 * (l >> 4);
+      for (int w = 0; w < NW; ++w) v += reinterpret_cast<const Acc*>(part + w * C::PART)[jf * 64 + l];
+    }
+    if (m >= p.M || n >= p.N) continue;
+    // K x N: where the lane's columns were moved back from the edge, column c of them is n - shift + c
+    const int base = KN ? min(n, p.N - 4) : n;
+    const float ra = DT == I8 ? p.alpha * p.ra[m] : p.alpha;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int col = base + e;
+      if (col < n || col >= p.N) continue;
+      const int64_t idx = (int64_t)m * p.ldc + col;
+      const float bj = (p.epi & EPI_BIAS) ? p.bias[col] : 0.0f;
+      float s = (float)v[e], scale = ra;
+      if constexpr (DT == I8) {
+        s = (s * ra) * p.rb[col];
+        scale = 1.0f;
+      }
+      auto put = [&](auto ct) {
+        constexpr int CT = decltype(ct)::value;
+        const float cin = p.beta != 0.0f ? load_as_float<CT>(p.C, idx) : 0.0f;
+        store_from_float<CT>(p.C, idx, epilogue_value<CT>(s, scale, p.beta, cin, bj, p.epi));
+      };
+      if (DT == I8 && c_type == F32) put(std::integral_constant<int, F32>{});
+      else if (DT == F16 || (DT == I8 && c_type == F16)) put(std::integral_constant<int, F16>{});
+      else put(std::integral_constant<int, BF16>{});
+    }
+  }
+}
+
+template <int DT, bool KN, int MF>
+hipError_t launch_stream_cfg(GemmParams p, const GroupArgs& ga, int c_type, int waves, hipStream_t s) {
+  using C = StreamCfg<DT, KN, MF>;
+  p.tiles_n = (p.N + C::BN - 1) / C::BN;
+  const int64_t grid = whole_rounds(max_row_tiles(p.M, ga.groups, C::BM) * p.tiles_n);
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((stream_kernel<DT, KN, MF>), dim3((unsigned)grid), dim3(64 * waves), waves * C::PART, s, p, ga, c_type);
+  return hipGetLastError();
+}
+
+// rows: 16, 32 or 64 rows of C per workgroup.
+template <int DT>
+hipError_t launch_stream_type(const GemmParams& p, const GroupArgs& ga, int c_type, bool kn, int rows, int waves,
+                              hipStream_t s) {
+  switch (rows * 2 + kn) {
+    case 32: return launch_stream_cfg<DT, false, 1>(p, ga, c_type, waves, s);
+    case 33: return launch_stream_cfg<DT, true, 1>(p, ga, c_type, waves, s);
+    case 64: return launch_stream_cfg<DT, false, 2>(p, ga, c_type, waves, s);
+    case 65: return launch_stream_cfg<DT, true, 2>(p, ga, c_type, waves, s);
+    case 128: return launch_stream_cfg<DT, false, 4>(p, ga, c_type, waves, s);
+    case 129: return launch_stream_cfg<DT, true, 4>(p, ga, c_type, waves, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace tgemm

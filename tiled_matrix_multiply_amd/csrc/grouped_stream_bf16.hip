@@ -1,0 +1,11 @@
+// Products for few rows per group, bf16 rows.
+#include "grouped_stream.hpp"
+
+namespace tgemm {
+
+hipError_t launch_stream_bf16(const GemmParams& p, const GroupArgs& ga, int c_type, bool kn, int rows, int waves,
+                            hipStream_t s) {
+  return launch_stream_type<BF16>(p, ga, c_type, kn, rows, waves, s);
+}
+
+}  // namespace tgemm

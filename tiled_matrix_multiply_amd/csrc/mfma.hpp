@@ -41,6 +41,7 @@ namespace tgemm {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -49,6 +50,8 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef __attribute__((address_space(3))) void lds_void;
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -116,6 +119,7 @@ template <int DT> struct MmaOp;
 template <> struct MmaOp<BF16> {
   static constexpr int KG = 16, CPL = 1;  // K per k-group, 16-byte chunks per lane
   using Frag = u32x4;
+  using Acc = f32x16;
   __device__ static __forceinline__ f32x16 run(const Frag& x, const Frag& y, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x),
                                                    __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
@@ -125,6 +129,7 @@ template <> struct MmaOp<BF16> {
 template <> struct MmaOp<F16> {
   static constexpr int KG = 16, CPL = 1;
   using Frag = u32x4;
+  using Acc = f32x16;
   __device__ static __forceinline__ f32x16 run(const Frag& x, const Frag& y, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, x),
                                                   __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
@@ -135,11 +140,23 @@ template <> struct MmaOp<F16> {
 template <> struct MmaOp<F32> {
   static constexpr int KG = 8, CPL = 1;
   using Frag = u32x4;
+  using Acc = f32x16;
   __device__ static __forceinline__ f32x16 run(const Frag& x, const Frag& y, f32x16 c) {
 #pragma unroll
     for (int s = 0; s < 4; ++s)
       c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(x[s]), __uint_as_float(y[s]), c, 0, 0, 0);
     return c;
+  }
+};
+
+// 8-bit integers: the sums are 32-bit integers, exact.
+template <> struct MmaOp<I8> {
+  static constexpr int KG = 32, CPL = 1;
+  using Frag = u32x4;
+  using Acc = i32x16;
+  __device__ static __forceinline__ i32x16 run(const Frag& x, const Frag& y, i32x16 c) {
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, x),
+                                                 __builtin_bit_cast(i32x4, y), c, 0, 0, 0);
   }
 };
 
@@ -167,6 +184,7 @@ struct MmaScaled {
   static constexpr bool FP4 = XT == E2M1, FP6 = is_fp6<XT>();
   static constexpr int KG = FP4 ? 32 : (FP6 ? 48 : 64), CPL = FP4 ? 1 : 2;
   using Frag = typename std::conditional<FP4, u32x4, u32x8>::type;
+  using Acc = f32x16;
   __device__ static __forceinline__ i32x8 widen(const Frag& x) {
     if constexpr (FP4) return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
     else return __builtin_bit_cast(i32x8, x);
@@ -207,16 +225,24 @@ constexpr int default_stages() { return TILE == 128 ? 3 : 2; }
 // (a pair protocol, below), and the other adds them and runs the epilogue.  With 0 (stream-K)
 // a persistent grid shares out the K tiles of all output tiles evenly, in contiguous runs that
 // may start and end inside a tile; the parts of a split tile meet through the workspace.
+// CT_: type of C (-1: the type that goes with DT_).  GR_: the tile to work on comes from the
+// caller (products grouped by expert, whose kernels find their group first), not from the
+// workgroup's index.  UNAL_: A, B and C may have any alignment: the copies go through registers
+// (unaligned 16-byte loads, element by element where a chunk leaves the matrix) instead of
+// straight into LDS.
 template <int DT_, int TILE_, int WM_, int WN_, bool A_MN_, bool B_MN_,
           int S_ = default_stages<TILE_>(), int BT_ = DT_, bool MX_ = false, int QB_ = 0,
-          int KS_ = 1, int BN_ = 0, int SK_ = 1>
+          int KS_ = 1, int BN_ = 0, int SK_ = 1, int CT_ = -1, bool GR_ = false, bool UNAL_ = false>
 struct MfmaCfg {
   static constexpr int DT = DT_, BT = BT_;
   static constexpr bool F8 = is_f8f6f4<DT_>(), MX = MX_;
   static_assert(DT_ == BT_ || (F8 && is_f8f6f4<BT_>()), "mixed types only in the 8-bit family");
   static_assert(!MX_ || F8, "block scales only with 8- and 4-bit inputs");
   using Op = typename std::conditional<F8, MmaScaled<BT_, DT_>, MmaOp<DT_>>::type;
-  static constexpr int CT = F8 ? BF16 : DT_;
+  static constexpr int CT = CT_ >= 0 ? CT_ : F8 ? BF16 : DT_;
+  static constexpr bool GR = GR_, UNAL = UNAL_;
+  static_assert(!UNAL_ || (KS_ == 1 && SK_ == 1 && !MX_ && QB_ == 0 && S_ == 2 && !is_fp6<DT_>()),
+                "copies through registers: plain inputs, two stages, no split");
   static constexpr int BM = TILE_, BN = BN_ ? BN_ : TILE_;
   static constexpr int KS = KS_, SK = SK_;
   static_assert(SK_ == 1 || ((SK_ == 2 || SK_ == 0) && KS_ == 1 && !MX_ && QB_ == 0),
@@ -364,6 +390,17 @@ struct SkSeg {
   int tile, kb, ke, part, parts, first_w;
 };
 
+// Tile `bid` of tiles_m x tiles_n in groups of TILE_GROUP_M tile rows.
+struct TilePos {
+  int tm, tn;
+};
+__device__ __forceinline__ TilePos tile_pos(int bid, int tiles_m, int tiles_n) {
+  const int per_group = TILE_GROUP_M * tiles_n;
+  const int first_m = (bid / per_group) * TILE_GROUP_M;
+  const int gsz = min(tiles_m - first_m, TILE_GROUP_M);
+  return TilePos{first_m + (bid % per_group) % gsz, (bid % per_group) / gsz};
+}
+
 // Workspace slot of stream-K contributor `part` of a tile whose first contributor is workgroup
 // w0: each workgroup has two slots, 2 w for the segment its run starts with (the end of a
 // tile) and 2 w + 1 for the one its run ends with (the start of a tile, part 0).
@@ -373,9 +410,10 @@ __device__ __forceinline__ int64_t sk_slot(int w0, int part) {
 
 // The work of one workgroup on one output tile (or, with stream-K, one segment of its K tiles),
 // from the copies of its first K tile to the stores of its epilogue.
+// smem: C::LDS_BYTES of LDS, 1024-byte aligned.  at: the tile, where the caller knows it (GR).
 template <class C>
-__device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS_BYTES];
+__device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, uint8_t* const smem,
+                                          const TilePos at = TilePos{}) {
   using Op = typename C::Op;
   using OA = Operand<C, true>;
   using OB = Operand<C, false>;
@@ -407,7 +445,7 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
   int khalf = 0;  // which part of the K tiles this workgroup takes (K split across workgroups)
   if constexpr (C::SK == 0) {
     bid = sg.tile;
-  } else {
+  } else if constexpr (!C::GR) {
     const int T = p.tiles_m * p.tiles_n;
     const int U = T * C::SK;  // workgroups
     if ((U & 7) == 0) bid = (bid & 7) * (U >> 3) + (bid >> 3);
@@ -417,11 +455,8 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
     }
   }
   const int tile_id = bid;
-  const int per_group = TILE_GROUP_M * p.tiles_n;
-  const int first_m = (bid / per_group) * TILE_GROUP_M;
-  const int gsz = min(p.tiles_m - first_m, TILE_GROUP_M);
-  const int tm = first_m + (bid % per_group) % gsz;
-  const int tn = (bid % per_group) / gsz;
+  const TilePos pos = C::GR ? at : tile_pos(bid, p.tiles_m, p.tiles_n);
+  const int tm = pos.tm, tn = pos.tn;
   const int m0 = tm * C::BM, n0 = tn * C::BN;
   const int wm = wave / C::WN, wn = wave % C::WN;
 
@@ -473,6 +508,37 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
         buffer_load_lds16(r, l + C::NCW * i * 1024, vo[i % O::VP]);
       }
     }
+  };
+
+  // Copies through registers (UNAL): the chunks of one K tile that this lane copies, as loaded.
+  u32x4 chA[C::UNAL ? OA::PER_WAVE : 1], chB[C::UNAL ? OB::PER_WAVE : 1];
+  auto load_chunks = [&](auto opnd, const uint8_t* mat, int64_t ld, int x0, int x_end, int k0, u32x4* dst) {
+    using O = decltype(opnd);
+    const int r0 = O::MN ? k0 : x0, r_end = O::MN ? p.K : x_end;
+    const int c0 = O::MN ? x0 : k0, c_end = O::MN ? x_end : p.K;
+#pragma unroll
+    for (int i = 0; i < O::PER_WAVE; ++i) {
+      int r, c;
+      O::chunk_of(cw + C::NCW * i, lane, r, c);
+      const int64_t gr = (int64_t)r0 + r, gc = (int64_t)c0 + c * O::CE;
+      u32x4 v = u32x4{0u, 0u, 0u, 0u};
+      if (gr < r_end && gc < c_end) {
+        const uint8_t* src = mat + (gr * ld + gc) * ES;
+        if (gc + O::CE <= c_end) __builtin_memcpy(&v, src, 16);
+        else v = load_partial<ES>(src, (int)(c_end - gc));
+      }
+      dst[i] = v;
+    }
+  };
+  auto store_chunks = [&](auto opnd, const u32x4* src, int buf) {
+    using O = decltype(opnd);
+#pragma unroll
+    for (int i = 0; i < O::PER_WAVE; ++i)
+      *reinterpret_cast<u32x4*>(gsm + O::LDS_OFF + buf * O::BUF_BYTES + (cw + C::NCW * i) * 1024 + lane * 16) = src[i];
+  };
+  auto load_tile_chunks = [&](int kt) {
+    load_chunks(OA{}, Ag, p.lda, m0, p.M, kt * C::BKE, chA);
+    load_chunks(OB{}, Bg, p.ldb, n0, p.N, kt * C::BKE, chB);
   };
 
   // Issue the direct copies of K tile kt of A (into A buffer buf) or of B (into B buffer buf).
@@ -596,7 +662,7 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
     } else if constexpr (ES == 1) {
       const int q = lane >> 4, sl = lane & 15;
       const int n = wbase + f * 32 + 16 * (q & 1) + 8 * (sl & 1);
-      const int k = 16 * (q >> 1) + (sl >> 1);  // lane half h: k 16h .. (see the op layout)
+      const int k = 16 * (q >> 1) + (sl >> 1);  // lane half h: k 16h .. (see the op layouts)
       v = k * O::RB + (((n >> 4) ^ O::mswz(k)) << 4) + (n & 15);
     } else {
       const int n = wbase + f * 32 + lrow;
@@ -656,6 +722,14 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
         out[2 * t] = d[0];
         out[2 * t + 1] = d[1];
       }
+    } else if constexpr (C::DT == I8) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {  // bytes 8t .. 8t+7: k 16 h + 8 t + 0..7 of the k-group
+        const uint8_t* a = s + mb[f] + (g * 32 + 8 * t) * O::RB;
+        const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)a);
+        out[2 * t] = (uint32_t)v[0];
+        out[2 * t + 1] = (uint32_t)v[1];
+      }
     } else if constexpr (ES == 1) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -687,13 +761,13 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
     for (int f = 0; f < C::FN; ++f) mbB[f] = mbase(OB{}, wn * C::WTN, f);
   }
 
-  f32x16 acc[C::FM][C::FN];
+  typename Op::Acc acc[C::FM][C::FN];
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
 #pragma unroll
     for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
   // Fragment schedules.  A tile is multiplied in G k-groups; in each, every wave issues the
   // FM x FN multiplies of its accumulator grid.
@@ -860,7 +934,7 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
   const int KT = C::KS == 1 ? KT_SK : (KT_ALL - kg + C::KS - 1) / C::KS;
   auto tile_of = [&](int i) { return C::KS == 1 ? kbeg + i : i * C::KS + kg; };
   const bool need_fix = (p.epi & (FIX_A | FIX_B)) != 0;
-  constexpr int NL = OA::PER_WAVE + (C::QB ? 0 : OB::PER_WAVE);  // data copies per copying wave per K tile
+  constexpr int NL = C::UNAL ? 0 : OA::PER_WAVE + (C::QB ? 0 : OB::PER_WAVE);  // data copies per copying wave per K tile
   const int nl = copier ? NL : 0;                                 // ... by this wave
   constexpr int NWL = (C::BM + C::BN) / 64;         // 64-row scale wave-loads per chunk
   constexpr int SPW = NWL > C::NCW ? NWL / C::NCW : 1;  // ... issued by each copying wave
@@ -889,6 +963,13 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
   };
   auto issue = [&](int it, int buf) {  // the tile of iteration it
     const int kt = tile_of(it);
+    if constexpr (C::UNAL) {
+      // the chunks loaded one tile ago, and the loads of the next tile's
+      store_chunks(OA{}, chA, buf);
+      store_chunks(OB{}, chB, buf);
+      if (it + 1 < KT) load_tile_chunks(kt + 1);
+      return;
+    }
     if constexpr (C::MX)
       if (kt % C::TPC == 0) issue_scales(kt / C::TPC);
     if constexpr (!C::QB) issue_b(kt, buf);
@@ -1025,6 +1106,8 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) qstore_part(q0, 0, i);
   }
+  if constexpr (C::UNAL)
+    if (KT > 0) load_tile_chunks(0);
 #pragma unroll
   for (int t = 0; t < C::S; ++t)
     if (t < KT) issue(t, t);
@@ -1109,11 +1192,12 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
   if constexpr (C::KS > 1) {
     // K split: groups 1 .. KS-1 hand their accumulators to group 0 through LDS (wave by wave,
     // float4 by float4, consecutive lanes 16 bytes apart), which adds them and stores.
-    constexpr int NF = C::FM * C::FN * 4;  // float4 pieces per lane
-    float4* const part = reinterpret_cast<float4*>(smem);
+    constexpr int NF = C::FM * C::FN * 4;  // 16-byte pieces per lane
+    using A4 = typename std::conditional<C::DT == I8, i32x4, f32x4>::type;
+    A4* const part = reinterpret_cast<A4*>(smem);
     __syncthreads();  // every group is done with its stages
     if (kg > 0) {
-      float4* dst = part + ((kg - 1) * C::NW + wave) * NF * 64 + lane;
+      A4* dst = part + ((kg - 1) * C::NW + wave) * NF * 64 + lane;
 #pragma unroll
       for (int i = 0; i < C::FM; ++i)
 #pragma unroll
@@ -1121,24 +1205,24 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             dst[((i * C::FN + j) * 4 + q) * 64] =
-                float4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                A4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     }
     __syncthreads();
     if (kg > 0) return;
 #pragma unroll
     for (int h = 1; h < C::KS; ++h) {
-      const float4* src = part + ((h - 1) * C::NW + wave) * NF * 64 + lane;
+      const A4* src = part + ((h - 1) * C::NW + wave) * NF * 64 + lane;
 #pragma unroll
       for (int i = 0; i < C::FM; ++i)
 #pragma unroll
         for (int j = 0; j < C::FN; ++j)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const float4 v = src[((i * C::FN + j) * 4 + q) * 64];
-            acc[i][j][4 * q] += v.x;
-            acc[i][j][4 * q + 1] += v.y;
-            acc[i][j][4 * q + 2] += v.z;
-            acc[i][j][4 * q + 3] += v.w;
+            const A4 v = src[((i * C::FN + j) * 4 + q) * 64];
+            acc[i][j][4 * q] += v[0];
+            acc[i][j][4 * q + 1] += v[1];
+            acc[i][j][4 * q + 2] += v[2];
+            acc[i][j][4 * q + 3] += v[3];
           }
     }
   }
@@ -1347,6 +1431,19 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
           }
     }
     const float alpha_e = hs * alpha, beta_e = hs * beta;
+    // 8-bit integers: the sum is scaled by alpha times its row's scale, then by its column's
+    float rj[C::FN][4][4];
+    if constexpr (C::DT == I8) {
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int rg = 0; rg < 4; ++rg)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int n = nw + 32 * j + 8 * rg + e;
+            rj[j][rg][e] = n < p.N ? p.rb[n] : 0.0f;
+          }
+    }
     // Output staging.  In the accumulator layout one store instruction would write 32 rows x
     // 16 bytes, 32 partial cache lines that L2 merges one request at a time.  Instead each wave
     // writes one row of accumulator tiles (32 x WTN outputs) into a private LDS region in that
@@ -1361,7 +1458,7 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
     static_assert(C::STG_OFF + C::NW * CHUNK <= C::LDS_BYTES, "output staging fits the K loop's LDS");
     uint8_t* const ostage = smem + C::STG_OFF + wave_u * CHUNK;
     const int m_w0 = m0 + wm * C::WTM, n_w0 = n0 + wn * C::WTN;
-    typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+    using u32x4_st = typename std::conditional<C::UNAL, u32x4_a2, u32x4_a4>::type;
     auto store_tile = [&](auto has_beta, auto has_gelu, auto is_edge) {
       constexpr bool HB = decltype(has_beta)::value, HG = decltype(has_gelu)::value;
       constexpr bool EDGE = decltype(is_edge)::value;
@@ -1369,6 +1466,7 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
       for (int i = 0; i < C::FM; ++i) {
         const int m = mw + 32 * i;                     // this lane's row (beta != 0 loads)
         const int64_t row = (int64_t)m * p.ldc;
+        const float ra = C::DT == I8 ? alpha_e * (m < p.M ? p.ra[m] : 0.0f) : 0.0f;
         float cin[C::FN][4][4];
         if constexpr (HB) {
 #pragma unroll
@@ -1377,8 +1475,8 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
             for (int rg = 0; rg < 4; ++rg) {
               const int n = nw + 32 * j + 8 * rg;
               const int64_t idx = row + n;
-              if (EDGE && !(m < p.M && n + 3 < p.N)) {
-                // a run of four that leaves the matrix: element by element
+              if (C::UNAL || (EDGE && !(m < p.M && n + 3 < p.N))) {
+                // a run of four that leaves the matrix, or of any alignment: element by element
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                   cin[j][rg][e] = (m < p.M && n + e < p.N) ? load_as_float<C::CT>(p.C, idx + e) : 0.0f;
@@ -1402,7 +1500,9 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float x = fmaf(alpha_e, acc[i][j][rg * 4 + e], bj[j][rg][e]);
+              float x;
+              if constexpr (C::DT == I8) x = fmaf((float)acc[i][j][rg * 4 + e] * ra, rj[j][rg][e], bj[j][rg][e]);
+              else x = fmaf(alpha_e, acc[i][j][rg * 4 + e], bj[j][rg][e]);
               if constexpr (HB) x = fmaf(beta_e, cin[j][rg][e], x);
               if constexpr (HG) {
                 if constexpr (C::CT == F32) x = gelu_out<C::CT>(x);
@@ -1423,7 +1523,7 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
           if (!EDGE || (gm < p.M && gn + EPG <= p.N)) {
             // non-temporal: C is not read again here, and lines the L2 does not keep dirty
             // need no write-back when the kernel ends (1.3 us less per 4096^3 launch)
-            __builtin_nontemporal_store(val, reinterpret_cast<u32x4_a4*>(dst));
+            __builtin_nontemporal_store(val, reinterpret_cast<u32x4_st*>(dst));
           } else if (gm < p.M && gn < p.N) {
             // the granule that straddles column N: its elements up to N one by one
             for (int e = 0; e < p.N - gn; ++e) {
@@ -1450,8 +1550,9 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg) {
 
 template <class C>
 __global__ __launch_bounds__(C::NT) void gemm_mfma_kernel(GemmParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS_BYTES];
   if constexpr (C::SK != 0) {
-    mfma_tile<C>(p, SkSeg{});
+    mfma_tile<C>(p, SkSeg{}, smem);
   } else {
     // Stream-K: a persistent grid of G workgroups shares out the I = tiles x KT K tiles of the
     // product, workgroup L taking the run [floor(L I / G), floor((L+1) I / G)) of the tile-major
@@ -1494,7 +1595,7 @@ __global__ __launch_bounds__(C::NT) void gemm_mfma_kernel(GemmParams p) {
       // same barriers), and the previous segment is done with LDS.
       __syncthreads();
       if (threadIdx.x == 0) run[0] = t0 + ke;  // published by the segment's own barriers
-      mfma_tile<C>(p, SkSeg{t, kb, ke, L - w0, w1 - w0 + 1, w0});
+      mfma_tile<C>(p, SkSeg{t, kb, ke, L - w0, w1 - w0 + 1, w0}, smem);
     }
   }
 }
