@@ -31,10 +31,9 @@ typedef enum gemm_grouped_kernel {
      and B's matrices follow each other at whole multiples of 16 bytes (at most 2^23 a row), the
      rows and matrices of C at multiples of 4 elements. */
   GEMM_GROUPED_MFMA_64 = 2,      /* 64x64 tile, the K loop split between two groups of waves */
-  GEMM_GROUPED_MFMA_128 = 3,     /* 128x128 tile, likewise */
-  GEMM_GROUPED_MFMA_256x128 = 4, /* 256x128 tile */
-  GEMM_GROUPED_MFMA_256 = 5,     /* 256x256 tile */
-  GEMM_GROUPED_STREAM = 6,       /* few rows a group (decoding): weights streamed through registers,
+  GEMM_GROUPED_MFMA_128 = 3,     /* 128x128 tile */
+  GEMM_GROUPED_MFMA_256 = 4,     /* 256x256 tile, with 128x128 ones where rows or rounds end */
+  GEMM_GROUPED_STREAM = 5,       /* few rows a group (decoding): weights streamed through registers,
                                     16 to 64 rows a tile, any alignment; rows of A and B of at most
                                     2^23 bytes, N >= 4 for a B stored K x N; not the gradient */
 } gemm_grouped_kernel_t;

@@ -65,11 +65,10 @@ GEMM_GROUPED_AUTO = 0
 GEMM_GROUPED_ANY = 1
 GEMM_GROUPED_MFMA_64 = 2
 GEMM_GROUPED_MFMA_128 = 3
-GEMM_GROUPED_MFMA_256x128 = 4
-GEMM_GROUPED_MFMA_256 = 5
-GEMM_GROUPED_STREAM = 6
-GROUPED_KERNEL_NAME = {0: "auto", 1: "any", 2: "mfma_64", 3: "mfma_128", 4: "mfma_256x128",
-                       5: "mfma_256", 6: "stream"}
+GEMM_GROUPED_MFMA_256 = 4
+GEMM_GROUPED_STREAM = 5
+GROUPED_KERNEL_NAME = {0: "auto", 1: "any", 2: "mfma_64", 3: "mfma_128", 4: "mfma_256",
+                       5: "stream"}
 
 # Every symbol include/gemm_grouped.h declares.
 GROUPED_EXPORTS = ("gemm_run_grouped", "gemm_run_grouped_wgrad", "gemm_run_i8",

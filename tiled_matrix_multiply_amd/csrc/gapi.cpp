@@ -174,25 +174,31 @@ gemm_grouped_kernel_t pick(const GArgs& a, int cus) {
   if (a.wgrad) {
     if (!tiles_fit(a)) return GEMM_GROUPED_ANY;
     auto tiles = [&](int64_t bm, int64_t bn) { return (a.N + bm - 1) / bm * ((a.K + bn - 1) / bn) * a.groups; };
-    if (tiles(256, 256) >= cus) return GEMM_GROUPED_MFMA_256;
+    // large tiles from 5/8 of a round on: 5 groups of 1744 x 1424 (210 tiles) 16 us against 23 on
+    // 128 x 128 ones, 4 of 2608 x 704 (132) 18 against 16
+    if (8 * tiles(256, 256) >= 5 * cus) return GEMM_GROUPED_MFMA_256;
     if (tiles(128, 128) >= cus / 2) return GEMM_GROUPED_MFMA_128;
     return GEMM_GROUPED_MFMA_64;
   }
   const int64_t rows = (a.M + live_groups(a) - 1) / live_groups(a);
-  if (rows <= 64 && stream_fits(a)) return GEMM_GROUPED_STREAM;
+  // Few rows: what counts is the weights' bytes.  Few 64 x 64 tiles stream too: more waves share out
+  // K (1584 rows over 2 groups, N 80, K 5832, bf16 23 us against 30 on 64 x 64 tiles, 236 x 688 x
+  // 1824 fp16 9 against 13; 545 rows over 6 groups, N 984, K 1432, whose tiles fill most compute
+  // units, 19 against 13).
+  if (stream_fits(a) && (rows <= 64 || 4 * expected_tiles(a, 64, 64) <= cus)) return GEMM_GROUPED_STREAM;
   if (!tiles_fit(a)) return GEMM_GROUPED_ANY;
   if (expected_tiles(a, 256, 256) >= cus) return GEMM_GROUPED_MFMA_256;
-  if (expected_tiles(a, 128, 128) > cus && expected_tiles(a, 256, 128) <= cus) return GEMM_GROUPED_MFMA_256x128;
   if (16 * expected_tiles(a, 128, 128) >= 9 * cus) return GEMM_GROUPED_MFMA_128;
   return GEMM_GROUPED_MFMA_64;
 }
 
-int tile_of(gemm_grouped_kernel_t k) {  // GroupedTile
+int tile_of(const GArgs& a, gemm_grouped_kernel_t k, int cus) {  // GroupedTile
+  const bool few = !a.wgrad && expected_tiles(a, 64, 64) <= cus;  // one 64 x 64 tile a compute unit
   switch (k) {
-    case GEMM_GROUPED_MFMA_64: return 1;
+    case GEMM_GROUPED_ANY: return few ? 5 : 0;
+    case GEMM_GROUPED_MFMA_64: return few ? 4 : 1;
     case GEMM_GROUPED_MFMA_128: return 2;
-    case GEMM_GROUPED_MFMA_256x128: return 3;
-    case GEMM_GROUPED_MFMA_256: return 4;
+    case GEMM_GROUPED_MFMA_256: return 3;
     default: return 0;
   }
 }
@@ -205,7 +211,6 @@ gemm_status_t choose(const GArgs& a, int cus, gemm_grouped_kernel_t& k) {
     case GEMM_GROUPED_STREAM: return stream_fits(a) ? GEMM_OK : GEMM_ERR_UNSUPPORTED;
     case GEMM_GROUPED_MFMA_64:
     case GEMM_GROUPED_MFMA_128:
-    case GEMM_GROUPED_MFMA_256x128:
     case GEMM_GROUPED_MFMA_256: return tiles_fit(a) ? GEMM_OK : GEMM_ERR_UNSUPPORTED;
     default: return GEMM_ERR_INVALID_VALUE;
   }
@@ -233,15 +238,19 @@ gemm_status_t run_rows(gemm_handle_t h, gemm_grouped_kernel_t kernel, void* stre
   const bool kn = a.transB == 0;
   tgemm::DeviceGuard g(h->device);
   if (kernel == GEMM_GROUPED_STREAM) {
+    // rows of a workgroup: what a group has on average, less while there are compute units to spare
+    // (the weights are then read once more, from the L2, but by more waves)
     const int64_t avg = (a.M + live_groups(a) - 1) / live_groups(a);
-    const int rows = avg <= (a.groups == 1 ? 16 : 10) ? 16 : avg <= (a.groups == 1 ? 32 : 24) ? 32 : 64;
+    int rows = avg <= (a.groups == 1 ? 16 : 10) ? 16 : avg <= (a.groups == 1 ? 32 : 24) ? 32 : 64;
+    while (rows > 16 && expected_tiles(a, rows, kn ? 64 : 32) <= h->cu_count / 2) rows /= 2;
     if (!countable(tgemm::max_row_tiles(a.M, a.groups, rows), a.N, kn ? 64 : 32)) return GEMM_ERR_UNSUPPORTED;
-    const int waves = rows == 64 && kn ? 4 : 8;
+    const bool one = expected_tiles(a, rows, kn ? 64 : 32) <= h->cu_count;  // workgroup a compute unit
+    const int waves = rows == 64 && kn ? 4 : rows == 16 && one ? 16 : 8;  // (at most 64 KB of LDS)
     return status(a.i8              ? tgemm::launch_stream_i8(p, ga, a.ct, kn, rows, waves, s)
                   : a.at == GEMM_F16 ? tgemm::launch_stream_f16(p, ga, a.ct, kn, rows, waves, s)
                                      : tgemm::launch_stream_bf16(p, ga, a.ct, kn, rows, waves, s));
   }
-  const int tile = tile_of(kernel);
+  const int tile = tile_of(a, kernel, h->cu_count);
   if (!a.i8) return status(a.at == GEMM_F16 ? tgemm::launch_grouped_f16(p, ga, kn, tile, h->cu_count, s) : tgemm::launch_grouped_bf16(p, ga, kn, tile, h->cu_count, s));
   return status(a.ct == GEMM_F32   ? tgemm::launch_grouped_i8_f32(p, ga, kn, tile, h->cu_count, s)
                 : a.ct == GEMM_F16 ? tgemm::launch_grouped_i8_f16(p, ga, kn, tile, h->cu_count, s)
@@ -272,8 +281,8 @@ gemm_status_t run_wgrad(gemm_handle_t h, gemm_grouped_kernel_t kernel, void* str
   const tgemm::BiasGrad b{a.B, a.ldb, (int)a.N, 0, 0, dbias};
   const hipStream_t s = static_cast<hipStream_t>(stream);
   tgemm::DeviceGuard g(h->device);
-  return status(a.at == GEMM_F16 ? tgemm::launch_grouped_wgrad_f16(p, ga, b, a.ct, tile_of(kernel), s)
-                                 : tgemm::launch_grouped_wgrad_bf16(p, ga, b, a.ct, tile_of(kernel), s));
+  return status(a.at == GEMM_F16 ? tgemm::launch_grouped_wgrad_f16(p, ga, b, a.ct, tile_of(a, kernel, h->cu_count), s)
+                                 : tgemm::launch_grouped_wgrad_bf16(p, ga, b, a.ct, tile_of(a, kernel, h->cu_count), s));
 }
 
 gemm_status_t check_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, gemm_dtype_t xt, const void* Q,

@@ -8,7 +8,7 @@
 namespace tgemm {
 
 // Tiles of the launchers below.
-enum GroupedTile : int { GT_ANY = 0, GT_64 = 1, GT_128 = 2, GT_256x128 = 3, GT_256 = 4 };
+enum GroupedTile : int { GT_ANY = 0, GT_64 = 1, GT_128 = 2, GT_256 = 3, GT_64_DEEP = 4, GT_ANY_DEEP = 5 };
 
 template <class C>
 __global__ __launch_bounds__(C::NT) void grouped_rows_kernel(GemmParams p, GroupArgs ga) {
@@ -22,49 +22,66 @@ __global__ __launch_bounds__(C::NT) void grouped_rows_kernel(GemmParams p, Group
 // 256 x 256 tiles (F) with 128 x 128 ones (Q) where the large would waste the chip:
 //  * a group's last rows, if at most 128 of them are left over, are tiles of 128 rows;
 //  * of the large tiles that do not fill a whole round of the compute units, each is split into
-//    four if the round gets shorter that way.  A split tile costs about 0.3 of a large one (its K
-//    loop is shared by two groups of waves), which decides: the time of the last rounds is
-//    estimated both ways in tenths of a large tile, small ones filling the holes of a started
-//    round three to a hole.
-// Large tiles come first, so that the small ones end the launch.
+//    four if the round gets shorter that way.
+// A small tile takes about 0.4 of a large one's time (bf16, K = 2048: 22 and 54 us), which decides:
+// the time of the last rounds is estimated both ways in tenths of a large tile, small ones filling
+// the holes of a started round two to a hole.  Large tiles come first, so that the small ones end
+// the launch.  Measured (4096 rows over 8 groups, N 4096, K 2048, bf16; 8190 over 16, N 2048, K
+// 4096, fp16): 115 and 222 us with large tiles alone, 87 and 171 mixed.
+__host__ __device__ __forceinline__ int large_rows(int rows) { return (int)(((int64_t)rows + 127) >> 8); }
+__host__ __device__ __forceinline__ int small_rows(int rows) { return (rows & 255) && (rows & 255) <= 128 ? 1 : 0; }
+// How many of nl large tiles to split, beside ns small ones.
+__host__ __device__ __forceinline__ int tiles_to_split(int nl, int ns, int cus) {
+  const int rounds = nl / cus, rest = nl - rounds * cus;
+  const int over = ns - (rest ? 2 * (cus - rest) : 0);
+  const int whole = 10 * (rounds + (rest > 0)) + 4 * (((over > 0 ? over : 0) + cus - 1) / cus);
+  const int apart = 10 * rounds + 4 * (int)((ns + 4 * (int64_t)rest + cus - 1) / cus);
+  return apart < whole ? rest : 0;
+}
+
+// `workers`: the workgroups (a whole number of rounds of 8) that share out the small tiles.  A
+// workgroup without work still has to wait for its LDS, so the grid holds no more of them than the
+// worst case of the large tiles asks for.
 template <class F, class Q>
-__global__ __launch_bounds__(512) void grouped_rows_mixed_kernel(GemmParams p, GroupArgs ga, int cus) {
+__global__ __launch_bounds__(512) void grouped_rows_mixed_kernel(const GemmParams p0, GroupArgs ga, int cus, int workers) {
   static_assert(F::NT == 512 && Q::NT == 512 && F::BM == 256 && Q::BM == 128, "two tiles of one workgroup size");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[F::LDS_BYTES > Q::LDS_BYTES ? F::LDS_BYTES : Q::LDS_BYTES];
-  const Groups gs(ga, p.M, threadIdx.x & 63);
-  auto large = [](int rows) { return (int)(((int64_t)rows + 127) >> 8); };
-  auto small = [](int rows) { return (rows & 255) && (rows & 255) <= 128 ? 1 : 0; };
-  const int tn = (p.N + 255) >> 8, tn_small = (p.N + 127) >> 7;
-  const int nl = gs.total(large) * tn, ns = gs.total(small) * tn_small;
-  const int rounds = nl / cus, rest = nl - rounds * cus;
-  const int whole = 10 * (rounds + (rest > 0)) + 3 * ((max(0, ns - (rest ? 3 * (cus - rest) : 0)) + cus - 1) / cus);
-  const int apart = 10 * rounds + 3 * ((ns + 4 * rest + cus - 1) / cus);
-  const int split = __builtin_amdgcn_readfirstlane(apart < whole ? rest : 0), kept = nl - split;
-  int bid = (int)blockIdx.x;
-  const int first_small = (kept + 7) & ~7;
+  const Groups gs(ga, p0.M, threadIdx.x & 63);
+  const int tn = (int)(((int64_t)p0.N + 255) >> 8), tn_small = (int)(((int64_t)p0.N + 127) >> 7);
+  const int nl = gs.total(large_rows) * tn, ns = gs.total(small_rows) * tn_small;
+  const int split = __builtin_amdgcn_readfirstlane(tiles_to_split(nl, ns, cus)), kept = nl - split;
+  const int first_small = (kept + 7) & ~7, bid = (int)blockIdx.x;
   if (bid < first_small) {
     const int t = xcd_item(bid, kept);
     if (t < 0) return;
-    const GroupItem it = gs.find(large, tn, t);
+    const GroupItem it = gs.find(large_rows, tn, t);
+    GemmParams p = p0;
     enter_group<F::ES, DTypeInfo<F::CT>::bytes>(p, ga, it.group, it.row0, it.rows);
-    mfma_tile<F>(p, SkSeg{}, smem, tile_pos(it.local, large(it.rows), tn));
+    mfma_tile<F>(p, SkSeg{}, smem, tile_pos(it.local, large_rows(it.rows), tn));
     return;
   }
-  const int t = xcd_item(bid - first_small, 4 * split + ns);
-  if (t < 0) return;
-  GroupItem it;
-  TilePos at;
-  if (t < 4 * split) {
-    it = gs.find(large, tn, kept + (t >> 2));
-    at = tile_pos(it.local, large(it.rows), tn);
-    at = TilePos{2 * at.tm + (t & 1), 2 * at.tn + ((t >> 1) & 1)};
-    if (128 * at.tm >= it.rows || 128 * at.tn >= p.N) return;
-  } else {
-    it = gs.find(small, tn_small, t - 4 * split);
-    at = TilePos{2 * large(it.rows), it.local};
+  if (bid - first_small >= workers) return;
+  const int pieces = 4 * split + ns;
+  for (int base = 0; base < pieces; base += workers) {
+    const int i = xcd_item(bid - first_small, min(workers, pieces - base));
+    if (i < 0) return;
+    const int t = base + i;
+    GroupItem it;
+    TilePos at;
+    if (t < 4 * split) {
+      it = gs.find(large_rows, tn, kept + (t >> 2));
+      at = tile_pos(it.local, large_rows(it.rows), tn);
+      at = TilePos{2 * at.tm + (t & 1), 2 * at.tn + ((t >> 1) & 1)};
+    } else {
+      it = gs.find(small_rows, tn_small, t - 4 * split);
+      at = TilePos{2 * large_rows(it.rows), it.local};
+    }
+    if (128 * at.tm >= it.rows || 128 * at.tn >= p0.N) continue;  // a quarter past the edge
+    if (base) __syncthreads();  // the last tile's output staging has been read
+    GemmParams p = p0;
+    enter_group<Q::ES, DTypeInfo<Q::CT>::bytes>(p, ga, it.group, it.row0, it.rows);
+    mfma_tile<Q>(p, SkSeg{}, smem, at);
   }
-  enter_group<Q::ES, DTypeInfo<Q::CT>::bytes>(p, ga, it.group, it.row0, it.rows);
-  mfma_tile<Q>(p, SkSeg{}, smem, at);
 }
 
 template <int DT, int NT>
@@ -169,15 +186,26 @@ hipError_t launch_rows_cfg(GemmParams p, const GroupArgs& ga, hipStream_t s) {
 
 template <class F, class Q>
 hipError_t launch_mixed_cfg(GemmParams p, const GroupArgs& ga, int cus, hipStream_t s) {
-  const int64_t rows = max_row_tiles(p.M, ga.groups, 256), live = ga.groups < p.M ? ga.groups : p.M;
-  const int64_t grid = whole_rounds(rows * ((p.N + 255) / 256)) +
-                       whole_rounds(4 * (int64_t)cus + live * ((p.N + 127) / 128));
+  const int64_t tn = ((int64_t)p.N + 255) / 256, tn_small = ((int64_t)p.N + 127) / 128;
+  int64_t large, small = cus;
+  if (ga.offsets) {
+    const int64_t live = ga.groups < p.M ? ga.groups : p.M;
+    large = (p.M + 127 * live) / 256 * tn;
+  } else {  // one group: exactly
+    const int64_t nl = large_rows(p.M) * tn, ns = small_rows(p.M) * tn_small;
+    const int split = tiles_to_split((int)nl, (int)ns, cus);
+    large = nl - split;
+    small = 4 * (int64_t)split + ns;
+  }
+  if (small > cus) small = cus;
+  const int64_t workers = whole_rounds(small), grid = whole_rounds(large) + workers;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  if (grid == 0) return hipSuccess;
   constexpr int CE = 16 / F::ES;
   static_assert(F::BKE == Q::BKE, "one K tile");
   if (p.K % F::BKE) p.epi |= FIX_A;
   if (F::B_MN ? p.N % CE : p.K % F::BKE) p.epi |= FIX_B;
-  hipLaunchKernelGGL((grouped_rows_mixed_kernel<F, Q>), dim3((unsigned)grid), dim3(512), 0, s, p, ga, cus);
+  hipLaunchKernelGGL((grouped_rows_mixed_kernel<F, Q>), dim3((unsigned)grid), dim3(512), 0, s, p, ga, cus, (int)workers);
   return hipGetLastError();
 }
 
@@ -201,18 +229,33 @@ hipError_t launch_wgrad_cfg(GemmParams p, const GroupArgs& ga, BiasGrad b, hipSt
   return hipGetLastError();
 }
 
-// MfmaCfg of a tile: B_MN / A_MN: stored contiguous along N / M.
-template <int DT, int CT, bool A_MN, bool B_MN, int TILE>
-struct GroupedCfg {
-  using T = typename std::conditional<
-      TILE == GT_ANY, MfmaCfg<DT, 64, 2, 2, A_MN, B_MN, 2, DT, false, 0, 1, 0, 1, CT, true, true>,
-      typename std::conditional<
-          TILE == GT_64, MfmaCfg<DT, 64, 2, 2, A_MN, B_MN, 2, DT, false, 0, 2, 0, 1, CT, true>,
-          typename std::conditional<
-              TILE == GT_128, MfmaCfg<DT, 128, 2, 2, A_MN, B_MN, 2, DT, false, 0, 2, 0, 1, CT, true>,
-              typename std::conditional<
-                  TILE == GT_256x128, MfmaCfg<DT, 256, 4, 2, A_MN, B_MN, 2, DT, false, 0, 1, 128, 1, CT, true>,
-                  MfmaCfg<DT, 256, 2, 4, A_MN, B_MN, 2, DT, false, 0, 1, 0, 1, CT, true>>::type>::type>::type>::type;
+// MfmaCfg of a tile (B_MN / A_MN: stored contiguous along N / M).
+//  * any alignment: each K tile waits for its loads and its LDS stores in turn; deep, four groups
+//    of waves split K, for when a compute unit has one tile at most (37 x 4104 x 4112 in 8 bits 37
+//    against 78 us, but 4096^3 226 against 147);
+//  * 64 x 64: two groups split K; deep, four stages each (one workgroup a compute unit) instead
+//    of two (two workgroups), for when there is no second tile to run beside the first: 1584 rows
+//    over 2 groups, N 80, K 5832, bf16, 31 against 40 us, but 545 tiles 39 against 33;
+//  * 128 x 128: four stages, eight waves: at K = 2048 (bf16) a tile takes 22 us, against 26 with K
+//    split between two groups of four waves with two stages each.
+template <int DT, int CT, bool A_MN, bool B_MN, int TILE> struct GroupedCfg;
+template <int DT, int CT, bool A_MN, bool B_MN> struct GroupedCfg<DT, CT, A_MN, B_MN, GT_ANY> {
+  using T = MfmaCfg<DT, 64, 2, 2, A_MN, B_MN, 2, DT, false, 0, 1, 0, 1, CT, true, true>;
+};
+template <int DT, int CT, bool A_MN, bool B_MN> struct GroupedCfg<DT, CT, A_MN, B_MN, GT_ANY_DEEP> {
+  using T = MfmaCfg<DT, 64, 2, 2, A_MN, B_MN, 2, DT, false, 0, 4, 0, 1, CT, true, true>;
+};
+template <int DT, int CT, bool A_MN, bool B_MN> struct GroupedCfg<DT, CT, A_MN, B_MN, GT_64> {
+  using T = MfmaCfg<DT, 64, 2, 2, A_MN, B_MN, 2, DT, false, 0, 2, 0, 1, CT, true>;
+};
+template <int DT, int CT, bool A_MN, bool B_MN> struct GroupedCfg<DT, CT, A_MN, B_MN, GT_64_DEEP> {
+  using T = MfmaCfg<DT, 64, 2, 2, A_MN, B_MN, 4, DT, false, 0, 2, 0, 1, CT, true>;
+};
+template <int DT, int CT, bool A_MN, bool B_MN> struct GroupedCfg<DT, CT, A_MN, B_MN, GT_128> {
+  using T = MfmaCfg<DT, 128, 2, 4, A_MN, B_MN, 4, DT, false, 0, 1, 0, 1, CT, true>;
+};
+template <int DT, int CT, bool A_MN, bool B_MN> struct GroupedCfg<DT, CT, A_MN, B_MN, GT_256> {
+  using T = MfmaCfg<DT, 256, 2, 4, A_MN, B_MN, 2, DT, false, 0, 1, 0, 1, CT, true>;
 };
 
 template <int DT, int CT, bool B_MN>
@@ -221,21 +264,22 @@ hipError_t launch_mixed_type(const GemmParams& p, const GroupArgs& ga, int cus, 
                           typename GroupedCfg<DT, CT, false, B_MN, GT_128>::T>(p, ga, cus, s);
 }
 
-template <int DT, int CT>
-hipError_t launch_rows_type(const GemmParams& p, const GroupArgs& ga, bool b_mn, int tile, int cus, hipStream_t s) {
-  switch (tile * 2 + b_mn) {
-    case GT_ANY * 2: return launch_rows_cfg<typename GroupedCfg<DT, CT, false, false, GT_ANY>::T>(p, ga, s);
-    case GT_ANY * 2 + 1: return launch_rows_cfg<typename GroupedCfg<DT, CT, false, true, GT_ANY>::T>(p, ga, s);
-    case GT_64 * 2: return launch_rows_cfg<typename GroupedCfg<DT, CT, false, false, GT_64>::T>(p, ga, s);
-    case GT_64 * 2 + 1: return launch_rows_cfg<typename GroupedCfg<DT, CT, false, true, GT_64>::T>(p, ga, s);
-    case GT_128 * 2: return launch_rows_cfg<typename GroupedCfg<DT, CT, false, false, GT_128>::T>(p, ga, s);
-    case GT_128 * 2 + 1: return launch_rows_cfg<typename GroupedCfg<DT, CT, false, true, GT_128>::T>(p, ga, s);
-    case GT_256x128 * 2: return launch_rows_cfg<typename GroupedCfg<DT, CT, false, false, GT_256x128>::T>(p, ga, s);
-    case GT_256x128 * 2 + 1: return launch_rows_cfg<typename GroupedCfg<DT, CT, false, true, GT_256x128>::T>(p, ga, s);
-    case GT_256 * 2: return launch_mixed_type<DT, CT, false>(p, ga, cus, s);
-    case GT_256 * 2 + 1: return launch_mixed_type<DT, CT, true>(p, ga, cus, s);
+template <int DT, int CT, bool B_MN>
+hipError_t launch_rows_layout(const GemmParams& p, const GroupArgs& ga, int tile, int cus, hipStream_t s) {
+  switch (tile) {
+    case GT_ANY: return launch_rows_cfg<typename GroupedCfg<DT, CT, false, B_MN, GT_ANY>::T>(p, ga, s);
+    case GT_ANY_DEEP: return launch_rows_cfg<typename GroupedCfg<DT, CT, false, B_MN, GT_ANY_DEEP>::T>(p, ga, s);
+    case GT_64: return launch_rows_cfg<typename GroupedCfg<DT, CT, false, B_MN, GT_64>::T>(p, ga, s);
+    case GT_64_DEEP: return launch_rows_cfg<typename GroupedCfg<DT, CT, false, B_MN, GT_64_DEEP>::T>(p, ga, s);
+    case GT_128: return launch_rows_cfg<typename GroupedCfg<DT, CT, false, B_MN, GT_128>::T>(p, ga, s);
+    case GT_256: return launch_mixed_type<DT, CT, B_MN>(p, ga, cus, s);
     default: return hipErrorInvalidValue;
   }
+}
+
+template <int DT, int CT>
+hipError_t launch_rows_type(const GemmParams& p, const GroupArgs& ga, bool b_mn, int tile, int cus, hipStream_t s) {
+  return b_mn ? launch_rows_layout<DT, CT, true>(p, ga, tile, cus, s) : launch_rows_layout<DT, CT, false>(p, ga, tile, cus, s);
 }
 
 template <int DT, int CT>
@@ -244,7 +288,6 @@ hipError_t launch_wgrad_type(const GemmParams& p, const GroupArgs& ga, const Bia
     case GT_ANY: return launch_wgrad_cfg<typename GroupedCfg<DT, CT, true, true, GT_ANY>::T>(p, ga, b, s);
     case GT_64: return launch_wgrad_cfg<typename GroupedCfg<DT, CT, true, true, GT_64>::T>(p, ga, b, s);
     case GT_128: return launch_wgrad_cfg<typename GroupedCfg<DT, CT, true, true, GT_128>::T>(p, ga, b, s);
-    case GT_256x128: return launch_wgrad_cfg<typename GroupedCfg<DT, CT, true, true, GT_256x128>::T>(p, ga, b, s);
     case GT_256: return launch_wgrad_cfg<typename GroupedCfg<DT, CT, true, true, GT_256>::T>(p, ga, b, s);
     default: return hipErrorInvalidValue;
   }

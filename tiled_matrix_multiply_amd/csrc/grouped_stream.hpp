@@ -47,7 +47,7 @@ struct StreamCfg {
 };
 
 template <int DT, bool KN, int MF>
-__global__ __launch_bounds__(512) void stream_kernel(GemmParams p, GroupArgs ga, int c_type) {
+__global__ __launch_bounds__(MF == 1 ? 1024 : 512) void stream_kernel(GemmParams p, GroupArgs ga, int c_type) {
   using C = StreamCfg<DT, KN, MF>;
   using Acc = typename std::conditional<DT == I8, s_i32x4, s_f32x4>::type;
   constexpr int ES = C::ES, CE = C::CE, KS = C::KS, NF = C::NF, U = C::U;
@@ -103,34 +103,46 @@ __global__ __launch_bounds__(512) void stream_kernel(GemmParams p, GroupArgs ga,
       for (int f = 0; f < NF; ++f) __builtin_memcpy(&t.b[4 * f], bs + ob[f], 16);
     }
   };
-  // The partial step after the last whole one: zeros past K on both sides.
+  // The partial step after the last whole one: zeros past K on both sides.  A lane's 16 bytes are
+  // whole, empty or, in at most one of the four quarters of the wave, cut.
   auto load_tail = [&](int s, Step& t) {
     const int64_t k = (int64_t)s * KS + q * CE;
     const int n = (int)min((int64_t)CE, max((int64_t)0, p.K - k));  // elements of this lane
-    auto elems = [&](const uint8_t* src, int count, s_u32x4& v) {
-      v = s_u32x4{0u, 0u, 0u, 0u};
+    auto chunk = [&](const uint8_t* src) {
+      s_u32x4 v = s_u32x4{0u, 0u, 0u, 0u};
+      if (n == CE) {
+        __builtin_memcpy(&v, src, 16);
+      } else if (n > 0) {
+        uint32_t x[CE];  // all loads first: past the end the last element once more
 #pragma unroll
-      for (int e = 0; e < CE; ++e)
-        if (e < count) {
-          const uint32_t x = ES == 1 ? src[e] : reinterpret_cast<const uint16_t*>(src)[e];
-          v[e * ES / 4] |= x << (8 * (e * ES % 4));
+        for (int e = 0; e < CE; ++e) {
+          const int at = min(e, n - 1);
+          x[e] = ES == 1 ? src[at] : reinterpret_cast<const uint16_t*>(src)[at];
         }
+#pragma unroll
+        for (int e = 0; e < CE; ++e) v[e * ES / 4] |= (e < n ? x[e] : 0u) << (8 * (e * ES % 4));
+      }
+      return v;
     };
 #pragma unroll
-    for (int f = 0; f < MF; ++f) elems(Ab + (int64_t)s * 64 + oa[f], n, t.a[f]);
+    for (int f = 0; f < MF; ++f) t.a[f] = chunk(Ab + (int64_t)s * 64 + oa[f]);
     if constexpr (KN) {
       const int64_t row = p.ldb * ES;
+      const uint8_t* const bs = Bb + (int64_t)s * KS * row + nl * ES;
 #pragma unroll
-      for (int i = 0; i < CE; ++i) {
-#pragma unroll
-        for (int d = 0; d < C::CB / 4; ++d) t.b[i * (C::CB / 4) + d] = 0u;
-        if (i < n) __builtin_memcpy(&t.b[i * (C::CB / 4)], Bb + ((int64_t)s * KS + i) * row + ob[0], C::CB);
+      for (int i = 0; i < CE; ++i) {  // past the end the matrix's last row once more
+        const int64_t kr = min((int64_t)q * CE + i, (int64_t)p.K - 1 - (int64_t)s * KS);
+        __builtin_memcpy(&t.b[i * (C::CB / 4)], bs + kr * row, C::CB);
       }
+#pragma unroll
+      for (int i = 0; i < CE; ++i)
+#pragma unroll
+        for (int d = 0; d < C::CB / 4; ++d)
+          if (i >= n) t.b[i * (C::CB / 4) + d] = 0u;
     } else {
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
-        s_u32x4 v;
-        elems(Bb + (int64_t)s * 64 + ob[f], n, v);
+        const s_u32x4 v = chunk(Bb + (int64_t)s * 64 + ob[f]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) t.b[4 * f + e] = v[e];
       }

@@ -241,8 +241,8 @@ struct MfmaCfg {
   using Op = typename std::conditional<F8, MmaScaled<BT_, DT_>, MmaOp<DT_>>::type;
   static constexpr int CT = CT_ >= 0 ? CT_ : F8 ? BF16 : DT_;
   static constexpr bool GR = GR_, UNAL = UNAL_;
-  static_assert(!UNAL_ || (KS_ == 1 && SK_ == 1 && !MX_ && QB_ == 0 && S_ == 2 && !is_fp6<DT_>()),
-                "copies through registers: plain inputs, two stages, no split");
+  static_assert(!UNAL_ || (SK_ == 1 && !MX_ && QB_ == 0 && S_ == 2 && !is_fp6<DT_>()),
+                "copies through registers: plain inputs, two stages");
   static constexpr int BM = TILE_, BN = BN_ ? BN_ : TILE_;
   static constexpr int KS = KS_, SK = SK_;
   static_assert(SK_ == 1 || ((SK_ == 2 || SK_ == 0) && KS_ == 1 && !MX_ && QB_ == 0),
@@ -410,7 +410,7 @@ __device__ __forceinline__ int64_t sk_slot(int w0, int part) {
 
 // The work of one workgroup on one output tile (or, with stream-K, one segment of its K tiles),
 // from the copies of its first K tile to the stores of its epilogue.
-// smem: C::LDS_BYTES of LDS, 1024-byte aligned.  at: the tile, where the caller knows it (GR).
+// smem: C::LDS_BYTES bytes of LDS, 1024-byte aligned.  at: the tile, where the caller knows it (GR).
 template <class C>
 __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, uint8_t* const smem,
                                           const TilePos at = TilePos{}) {
@@ -516,18 +516,39 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, ui
     using O = decltype(opnd);
     const int r0 = O::MN ? k0 : x0, r_end = O::MN ? p.K : x_end;
     const int c0 = O::MN ? x0 : k0, c_end = O::MN ? x_end : p.K;
+    // In each of the three ways all loads are issued before any is looked at.
+    int64_t gr[O::PER_WAVE], gc[O::PER_WAVE];
 #pragma unroll
     for (int i = 0; i < O::PER_WAVE; ++i) {
       int r, c;
       O::chunk_of(cw + C::NCW * i, lane, r, c);
-      const int64_t gr = (int64_t)r0 + r, gc = (int64_t)c0 + c * O::CE;
-      u32x4 v = u32x4{0u, 0u, 0u, 0u};
-      if (gr < r_end && gc < c_end) {
-        const uint8_t* src = mat + (gr * ld + gc) * ES;
-        if (gc + O::CE <= c_end) __builtin_memcpy(&v, src, 16);
-        else v = load_partial<ES>(src, (int)(c_end - gc));
+      gr[i] = (int64_t)r0 + r;
+      gc[i] = (int64_t)c0 + c * O::CE;
+    }
+    if ((int64_t)x0 + O::BX <= x_end && (int64_t)k0 + C::BKE <= p.K) {  // inside the matrix
+#pragma unroll
+      for (int i = 0; i < O::PER_WAVE; ++i) __builtin_memcpy(&dst[i], mat + (gr[i] * ld + gc[i]) * ES, 16);
+    } else if (c_end >= O::CE) {
+      // chunks past an edge are read from the last place inside, and what belongs to other rows and
+      // columns is shifted out: zeros come in
+#pragma unroll
+      for (int i = 0; i < O::PER_WAVE; ++i)
+        __builtin_memcpy(&dst[i], mat + (min(gr[i], (int64_t)r_end - 1) * ld + min(gc[i], (int64_t)c_end - O::CE)) * ES, 16);
+#pragma unroll
+      for (int i = 0; i < O::PER_WAVE; ++i) {
+        const int n = gr[i] < r_end ? (int)max((int64_t)0, min((int64_t)O::CE, c_end - gc[i])) : 0;
+        const int sh = (O::CE - n) * ES * 8;
+        const uint64_t lo = (uint64_t)dst[i][1] << 32 | dst[i][0], hi = (uint64_t)dst[i][3] << 32 | dst[i][2];
+        const uint64_t l2 = sh == 0 ? lo : sh < 64 ? (lo >> sh) | (hi << (64 - sh)) : sh < 128 ? hi >> (sh - 64) : 0;
+        const uint64_t h2 = sh < 64 ? hi >> sh : 0;
+        dst[i] = u32x4{(uint32_t)l2, (uint32_t)(l2 >> 32), (uint32_t)h2, (uint32_t)(h2 >> 32)};
       }
-      dst[i] = v;
+    } else {  // rows shorter than a chunk
+#pragma unroll
+      for (int i = 0; i < O::PER_WAVE; ++i) {
+        dst[i] = u32x4{0u, 0u, 0u, 0u};
+        if (gr[i] < r_end && gc[i] < c_end) dst[i] = load_partial<ES>(mat + (gr[i] * ld + gc[i]) * ES, (int)(c_end - gc[i]));
+      }
     }
   };
   auto store_chunks = [&](auto opnd, const u32x4* src, int buf) {
@@ -967,7 +988,7 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, ui
       // the chunks loaded one tile ago, and the loads of the next tile's
       store_chunks(OA{}, chA, buf);
       store_chunks(OB{}, chB, buf);
-      if (it + 1 < KT) load_tile_chunks(kt + 1);
+      if (it + 1 < KT) load_tile_chunks(tile_of(it + 1));
       return;
     }
     if constexpr (C::MX)
@@ -1107,7 +1128,7 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, ui
     for (int i = 0; i < 4; ++i) qstore_part(q0, 0, i);
   }
   if constexpr (C::UNAL)
-    if (KT > 0) load_tile_chunks(0);
+    if (KT > 0) load_tile_chunks(tile_of(0));
 #pragma unroll
   for (int t = 0; t < C::S; ++t)
     if (t < KT) issue(t, t);
@@ -1399,6 +1420,37 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, ui
   const int mw = m0 + wm * C::WTM + lrow;
   const int nw = n0 + wn * C::WTN + lhalf * 4;
   {
+    // 8-bit integers: the sums become fp32 in place, scaled by alpha times their row's scale, then
+    // by their column's; the rest of the epilogue is the other types'.
+    constexpr bool INT = C::DT == I8;
+    auto val = [&](int i, int j, int r) {
+      if constexpr (INT) return __int_as_float(acc[i][j][r]);
+      else return acc[i][j][r];
+    };
+    if constexpr (INT) {
+      float ra[C::FM];
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) ra[i] = full || mw + 32 * i < p.M ? p.ra[mw + 32 * i] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int rg = 0; rg < 4; ++rg) {
+          const int n = nw + 32 * j + 8 * rg;
+          float rb[4];
+          if (full) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) rb[e] = p.rb[n + e];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) rb[e] = n + e < p.N ? p.rb[n + e] : 0.0f;
+          }
+#pragma unroll
+          for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc[i][j][4 * rg + e] = __float_as_int(((float)acc[i][j][4 * rg + e] * (alpha * ra[i])) * rb[e]);
+        }
+    }
     // Interior tiles carry no masks.  The bias values of the lane's columns are fetched in one
     // batch (a single wait), each row's C values (beta != 0) likewise, and the element loop is
     // specialised on (beta != 0, GELU, edge) so that it carries no branches: this loop runs on
@@ -1430,20 +1482,7 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, ui
             bj[j][rg][e] = ((epi & EPI_BIAS) && n < p.N) ? hs * p.bias[n] : 0.0f;
           }
     }
-    const float alpha_e = hs * alpha, beta_e = hs * beta;
-    // 8-bit integers: the sum is scaled by alpha times its row's scale, then by its column's
-    float rj[C::FN][4][4];
-    if constexpr (C::DT == I8) {
-#pragma unroll
-      for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-        for (int rg = 0; rg < 4; ++rg)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int n = nw + 32 * j + 8 * rg + e;
-            rj[j][rg][e] = n < p.N ? p.rb[n] : 0.0f;
-          }
-    }
+    const float alpha_e = INT ? hs : hs * alpha, beta_e = hs * beta;
     // Output staging.  In the accumulator layout one store instruction would write 32 rows x
     // 16 bytes, 32 partial cache lines that L2 merges one request at a time.  Instead each wave
     // writes one row of accumulator tiles (32 x WTN outputs) into a private LDS region in that
@@ -1459,6 +1498,7 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, ui
     uint8_t* const ostage = smem + C::STG_OFF + wave_u * CHUNK;
     const int m_w0 = m0 + wm * C::WTM, n_w0 = n0 + wn * C::WTN;
     using u32x4_st = typename std::conditional<C::UNAL, u32x4_a2, u32x4_a4>::type;
+    const bool whole_lines = p.ldc * OES % 128 == 0 && reinterpret_cast<uintptr_t>(p.C) % 128 == 0;
     auto store_tile = [&](auto has_beta, auto has_gelu, auto is_edge) {
       constexpr bool HB = decltype(has_beta)::value, HG = decltype(has_gelu)::value;
       constexpr bool EDGE = decltype(is_edge)::value;
@@ -1466,7 +1506,6 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, ui
       for (int i = 0; i < C::FM; ++i) {
         const int m = mw + 32 * i;                     // this lane's row (beta != 0 loads)
         const int64_t row = (int64_t)m * p.ldc;
-        const float ra = C::DT == I8 ? alpha_e * (m < p.M ? p.ra[m] : 0.0f) : 0.0f;
         float cin[C::FN][4][4];
         if constexpr (HB) {
 #pragma unroll
@@ -1500,9 +1539,7 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, ui
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float x;
-              if constexpr (C::DT == I8) x = fmaf((float)acc[i][j][rg * 4 + e] * ra, rj[j][rg][e], bj[j][rg][e]);
-              else x = fmaf(alpha_e, acc[i][j][rg * 4 + e], bj[j][rg][e]);
+              float x = fmaf(alpha_e, val(i, j, rg * 4 + e), bj[j][rg][e]);
               if constexpr (HB) x = fmaf(beta_e, cin[j][rg][e], x);
               if constexpr (HG) {
                 if constexpr (C::CT == F32) x = gelu_out<C::CT>(x);
@@ -1522,8 +1559,17 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, ui
           uint8_t* dst = reinterpret_cast<uint8_t*>(p.C) + ((int64_t)gm * p.ldc + gn) * OES;
           if (!EDGE || (gm < p.M && gn + EPG <= p.N)) {
             // non-temporal: C is not read again here, and lines the L2 does not keep dirty
-            // need no write-back when the kernel ends (1.3 us less per 4096^3 launch)
-            __builtin_nontemporal_store(val, reinterpret_cast<u32x4_st*>(dst));
+            // need no write-back when the kernel ends (1.3 us less per 4096^3 launch).  Grouped
+            // products whose rows of C do not start on lines leave it to the L2 to put the two
+            // parts of a line together (gradients of 17 groups of 2064 x 3800 fp32: 136 us against
+            // 178; with whole lines, 8 of 4096 x 2048 bf16, non-temporal is 84 against 96)
+            if (!C::GR || whole_lines) __builtin_nontemporal_store(val, reinterpret_cast<u32x4_st*>(dst));
+            else {
+              // (around the store, so that the compiler cannot merge the two into a plain one)
+              asm volatile("");
+              *reinterpret_cast<u32x4_st*>(dst) = val;
+              asm volatile("");
+            }
           } else if (gm < p.M && gn < p.N) {
             // the granule that straddles column N: its elements up to N one by one
             for (int e = 0; e < p.N - gn; ++e) {
@@ -1535,7 +1581,10 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, ui
       }
     };
     auto store_any = [&](auto is_edge) {
-      if (beta != 0.0f) {
+      if constexpr (C::GR && C::A_MN) {  // a weight gradient has no GELU
+        if (beta != 0.0f) store_tile(std::true_type{}, std::false_type{}, is_edge);
+        else store_tile(std::false_type{}, std::false_type{}, is_edge);
+      } else if (beta != 0.0f) {
         if (epi & EPI_GELU) store_tile(std::true_type{}, std::true_type{}, is_edge);
         else store_tile(std::true_type{}, std::false_type{}, is_edge);
       } else {
