@@ -242,7 +242,7 @@ gemm_status_t run_rows(gemm_handle_t h, gemm_grouped_kernel_t kernel, void* stre
     // (the weights are then read once more, from the L2, but by more waves)
     const int64_t avg = (a.M + live_groups(a) - 1) / live_groups(a);
     int rows = avg <= (a.groups == 1 ? 16 : 10) ? 16 : avg <= (a.groups == 1 ? 32 : 24) ? 32 : 64;
-    while (rows > 16 && expected_tiles(a, rows, kn ? 64 : 32) <= h->cu_count / 2) rows /= 2;
+    while (rows > 16 && 4 * expected_tiles(a, rows, kn ? 64 : 32) <= 3 * h->cu_count) rows /= 2;
     if (!countable(tgemm::max_row_tiles(a.M, a.groups, rows), a.N, kn ? 64 : 32)) return GEMM_ERR_UNSUPPORTED;
     const bool one = expected_tiles(a, rows, kn ? 64 : 32) <= h->cu_count;  // workgroup a compute unit
     const int waves = rows == 64 && kn ? 4 : rows == 16 && one ? 16 : 8;  // (at most 64 KB of LDS)

@@ -189,9 +189,11 @@ __global__ __launch_bounds__(MF == 1 ? 1024 : 512) void stream_kernel(GemmParams
       for (int f = 0; f < MF; ++f) acc[j][f] = mma16<DT>(b[j], t.a[f], acc[j][f]);
   };
 
-  // Whole steps in blocks of U, block after block over the waves; then the last few steps one by
-  // one, and the partial step.
-  const int steps = p.K / KS, blocks = steps / U;
+  // Whole steps in blocks of U, block after block over the waves; the last few steps and the
+  // partial one go to one wave each, before its blocks.  Every load of the loop is unconditional
+  // and its place among the loads in flight known at compile time: a load inside a branch would
+  // make every wait behind it wait for all of them.
+  const int steps = p.K / KS, blocks = steps / U, rest = steps - blocks * U;
   Step x[U], y[U];
   auto load_block = [&](int b, Step (&t)[U]) {
 #pragma unroll
@@ -201,24 +203,29 @@ __global__ __launch_bounds__(MF == 1 ? 1024 : 512) void stream_kernel(GemmParams
 #pragma unroll
     for (int u = 0; u < U; ++u) mul(t[u]);
   };
-  int b = wave;
-  if (b < blocks) load_block(b, x);
-  while (b < blocks) {
-    const int b1 = b + NW, b2 = b1 + NW;
-    if (b1 < blocks) load_block(b1, y);
-    mul_block(x);
-    if (b1 >= blocks) break;
-    if (b2 < blocks) load_block(b2, x);
-    mul_block(y);
-    b = b2;
+  if (wave < rest) {
+    load(blocks * U + wave, y[0]);
+    mul(y[0]);
+  } else if (wave == rest && steps * KS < p.K) {
+    load_tail(steps, y[0]);
+    mul(y[0]);
   }
-  for (int s = blocks * U + wave; s < steps; s += NW) {
-    load(s, x[0]);
-    mul(x[0]);
-  }
-  if (steps * KS < p.K && wave == (steps - blocks * U) % NW) {
-    load_tail(steps, x[0]);
-    mul(x[0]);
+  if (wave < blocks) {
+    int b = wave;
+    load_block(b, x);
+    for (; b + 2 * NW < blocks; b += 2 * NW) {
+      load_block(b + NW, y);
+      mul_block(x);
+      load_block(b + 2 * NW, x);
+      mul_block(y);
+    }
+    if (b + NW < blocks) {
+      load_block(b + NW, y);
+      mul_block(x);
+      mul_block(y);
+    } else {
+      mul_block(x);
+    }
   }
 
   Acc* const mine = reinterpret_cast<Acc*>(part + wave * C::PART);
@@ -230,48 +237,55 @@ __global__ __launch_bounds__(MF == 1 ? 1024 : 512) void stream_kernel(GemmParams
 
   // Item i of 16 MF rows x BN columns in runs of four columns.  A lane of fragment (j, f) holds row
   // 16 f + l16 and, in register r, the fragment's row 4 q + r.
-  for (int i = threadIdx.x; i < NF * MF * 64; i += blockDim.x) {
-    int m, n;
-    Acc v = Acc{0, 0, 0, 0};
-    if constexpr (KN) {
-      const int r = i & 3, l = (i >> 2) & 63, f = i >> 8;
-      m = m0 + 16 * f + (l & 15);
-      n = n0 + 16 * (l >> 4) + 4 * r;
+  auto finish = [&](auto ct) {
+    constexpr int CT = decltype(ct)::value;
+    for (int i = threadIdx.x; i < NF * MF * 64; i += blockDim.x) {
+      int m, n;
+      const int r = i & 3, l = KN ? (i >> 2) & 63 : i & 63, jf = KN ? i >> 8 : i >> 6;
+      if constexpr (KN) {
+        m = m0 + 16 * jf + (l & 15);
+        n = n0 + 16 * (l >> 4) + 4 * r;
+      } else {
+        m = m0 + 16 * (jf % MF) + (l & 15);
+        n = n0 + 16 * (jf / MF) + 4 * (l >> 4);
+      }
+      if (m >= p.M || n >= p.N) continue;
+      // K x N: where the lane's columns were moved back from the edge, column e of them is base + e
+      const int base = KN ? min(n, p.N - 4) : n;
+      // all reads together, past the edge the last column once more
+      float bj[4], rb[4], cin[4];
+      const float ra = DT == I8 ? p.alpha * p.ra[m] : p.alpha;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int col = min(base + e, p.N - 1);
+        bj[e] = (p.epi & EPI_BIAS) ? p.bias[col] : 0.0f;
+        rb[e] = DT == I8 ? p.rb[col] : 1.0f;
+        cin[e] = p.beta != 0.0f ? load_as_float<CT>(p.C, (int64_t)m * p.ldc + col) : 0.0f;
+      }
+      Acc v = Acc{0, 0, 0, 0};
       for (int w = 0; w < NW; ++w) {
         const Acc* src = reinterpret_cast<const Acc*>(part + w * C::PART);
+        if constexpr (KN) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] += src[(j * MF + f) * 64 + l][r];
+          for (int j = 0; j < 4; ++j) v[j] += src[(j * MF + jf) * 64 + l][r];
+        } else {
+          v += src[jf * 64 + l];
+        }
       }
-    } else {
-      const int l = i & 63, jf = i >> 6;
-      m = m0 + 16 * (jf % MF) + (l & 15);
-      n = n0 + 16 * (jf / MF) + 4 * (l >> 4);
-      for (int w = 0; w < NW; ++w) v += reinterpret_cast<const Acc*>(part + w * C::PART)[jf * 64 + l];
-    }
-    if (m >= p.M || n >= p.N) continue;
-    // K x N: where the lane's columns were moved back from the edge, column c of them is n - shift + c
-    const int base = KN ? min(n, p.N - 4) : n;
-    const float ra = DT == I8 ? p.alpha * p.ra[m] : p.alpha;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int col = base + e;
-      if (col < n || col >= p.N) continue;
-      const int64_t idx = (int64_t)m * p.ldc + col;
-      const float bj = (p.epi & EPI_BIAS) ? p.bias[col] : 0.0f;
-      float s = (float)v[e], scale = ra;
-      if constexpr (DT == I8) {
-        s = (s * ra) * p.rb[col];
-        scale = 1.0f;
+      for (int e = 0; e < 4; ++e) {
+        const float s = DT == I8 ? ((float)v[e] * ra) * rb[e] : (float)v[e];
+        const float out = epilogue_value<CT>(s, DT == I8 ? 1.0f : ra, p.beta, cin[e], bj[e], p.epi);
+        if (base + e >= n && base + e < p.N) store_from_float<CT>(p.C, (int64_t)m * p.ldc + base + e, out);
       }
-      auto put = [&](auto ct) {
-        constexpr int CT = decltype(ct)::value;
-        const float cin = p.beta != 0.0f ? load_as_float<CT>(p.C, idx) : 0.0f;
-        store_from_float<CT>(p.C, idx, epilogue_value<CT>(s, scale, p.beta, cin, bj, p.epi));
-      };
-      if (DT == I8 && c_type == F32) put(std::integral_constant<int, F32>{});
-      else if (DT == F16 || (DT == I8 && c_type == F16)) put(std::integral_constant<int, F16>{});
-      else put(std::integral_constant<int, BF16>{});
     }
+  };
+  if constexpr (DT == I8) {
+    if (c_type == F32) finish(std::integral_constant<int, F32>{});
+    else if (c_type == F16) finish(std::integral_constant<int, F16>{});
+    else finish(std::integral_constant<int, BF16>{});
+  } else {
+    finish(std::integral_constant<int, DT>{});
   }
 }
 
