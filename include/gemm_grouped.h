@@ -47,7 +47,7 @@ typedef enum gemm_grouped_kernel {
  * fp32, groups x N, contiguous (NULL without GEMM_EPI_BIAS).  type: GEMM_F16 or GEMM_BF16, of
  * A, B and C; sums are fp32, rounded once.  Epilogue bits as gemm_run.  With the weights' other
  * transB, and C and A exchanged, the same call is the data gradient dA = dC op(B_g)^T.
- * Errors: as gemm_run, plus GEMM_ERR_INVALID_VALUE for groups < 0, stride_b < 0 or NULL offsets
+ * Errors: as gemm_run (dimensions of at most 2^31 - 1024), plus GEMM_ERR_INVALID_VALUE for groups < 0, stride_b < 0 or NULL offsets
  * with groups > 0, and GEMM_ERR_UNSUPPORTED for groups > 65535 or a kernel whose needs (see
  * gemm_grouped_kernel) do not hold.  M, N or groups of 0 enqueue nothing. */
 GEMM_API gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_grouped_kernel_t kernel,

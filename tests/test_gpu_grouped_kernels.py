@@ -4,6 +4,7 @@ kernel at any, and the sizes at which each one's tiles, K loops and column block
 import numpy as np
 import pytest
 
+import test_gpu_grouped as base
 from test_gpu_grouped import (DIMS, MANY, SIZES, check, dev, g, host, offsets_of, run_grouped,  # noqa: F401
                               run_i8, run_quantize, run_wgrad)
 
@@ -150,6 +151,34 @@ def test_kernels_that_do_not_fit(g):  # noqa: F811
         g.run_grouped_wgrad(A, B, C, off, groups=1, M=8, N=16, K=16, kernel=STREAM)
     torch.cuda.synchronize()
     assert (C == 1).all()
+
+
+@pytest.mark.parametrize("kernel", [0, 1] + TILES + [STREAM])
+def test_nothing_to_sum(g, kernel):  # noqa: F811
+    """K = 0: the epilogue of zero sums; a gradient without columns still has its bias gradient."""
+    for trans_b in (False, True):
+        run_grouped(g, [5, 0, 70], 48, 0, trans_b=trans_b, t="bf16", kernel=kernel, lda=8, ldb=48,
+                    stride=0, bias=True, do_gelu=True, beta=0.5)
+        run_i8(g, [5, 0, 70], 48, 0, trans_b=trans_b, ct="f16", kernel=kernel, lda=16, ldb=48, bias=True)
+    if kernel != STREAM:
+        import torch
+        D = torch.randn(9, 24, device="cuda").to(torch.bfloat16)
+        db = torch.full((2, 24), float("nan"), device="cuda")
+        g.run_grouped_wgrad(None, D, None, dev(np.array([0, 4, 9], dtype=np.int64)), groups=2, M=9, N=24,
+                            K=0, lda=8, ldc=24, dbias=db, kernel=kernel)
+        want = np.stack([host(D)[:4].sum(0), host(D)[4:].sum(0)])
+        size = np.stack([np.abs(host(D))[:4].sum(0), np.abs(host(D))[4:].sum(0)])
+        check(host(db), want, size, 9 * 2.0 ** -24, "f32", kernel)
+
+
+@pytest.mark.parametrize("kernel", TILES + [STREAM])
+def test_far_addresses(g, kernel):  # noqa: F811
+    base.test_grouped_far_addresses(g, kernel)
+
+
+@pytest.mark.parametrize("kernel", TILES + [STREAM])
+def test_infinities_stay_in_their_rows(g, kernel):  # noqa: F811
+    base.test_grouped_infinities_stay_in_their_rows(g, kernel)
 
 
 @pytest.mark.parametrize("t", ["bf16", "f16", "f32"])

@@ -28,7 +28,7 @@ hipError_t launch_quantize_rows(const void* X, int64_t ldx, int M, int K, int x_
 
 namespace {
 
-constexpr int64_t kMaxDim = 0x7fffffff;
+constexpr int64_t kMaxDim = 0x7fffffff - 1023;  // tile edges past a dimension still fit 31 bits
 constexpr int64_t kMaxGroups = 65535;
 constexpr int64_t kMaxK8 = 131071;  // 128 * 128 * K < 2^31
 
@@ -193,7 +193,9 @@ gemm_grouped_kernel_t pick(const GArgs& a, int cus) {
 }
 
 int tile_of(const GArgs& a, gemm_grouped_kernel_t k, int cus) {  // GroupedTile
-  const bool few = !a.wgrad && expected_tiles(a, 64, 64) <= cus;  // one 64 x 64 tile a compute unit
+  // one 64 x 64 tile a compute unit
+  const int64_t tiles = a.wgrad ? (a.N + 63) / 64 * ((a.K + 63) / 64) * a.groups : expected_tiles(a, 64, 64);
+  const bool few = tiles <= cus;
   switch (k) {
     case GEMM_GROUPED_ANY: return few ? 5 : 0;
     case GEMM_GROUPED_MFMA_64: return few ? 4 : 1;

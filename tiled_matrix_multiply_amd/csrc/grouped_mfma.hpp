@@ -140,7 +140,11 @@ __device__ __forceinline__ void bias_tile(const BiasGrad& b, const GroupArgs& ga
 // The weight gradient: p.M x p.N is the gradient as stored, p.A and p.B the rows it is the product
 // of, p.K all rows.  xcd: the tiles of each group are dealt out to the XCDs in contiguous ranges
 // (a group's rows decide its tiles' time, so whole groups are never given to one XCD); otherwise,
-// with too few tiles in a group for that, tile after tile.
+// with too few tiles in a group for that, tile after tile.  Groups with the most rows come first
+// (8 groups of 4096 x 2048 bf16 from 4096 uneven rows: 90 us in their own order, 84 so).
+// What bounds it with few rows to a group is the writing of the gradient, which the products do not
+// hide: those 8 groups take 30 us with no rows at all and 0.1 us more for each row of a group (53 us
+// for 512, 1.3 PFLOP/s).  16 groups of 4096 x 2048 from 16383 rows in fp32: 320 us, 0.5 GB written.
 template <class C>
 __global__ __launch_bounds__(C::NT) void grouped_wgrad_kernel(GemmParams p, GroupArgs ga, BiasGrad b, int xcd) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS_BYTES];
@@ -286,6 +290,8 @@ template <int DT, int CT>
 hipError_t launch_wgrad_type(const GemmParams& p, const GroupArgs& ga, const BiasGrad& b, int tile, hipStream_t s) {
   switch (tile) {
     case GT_ANY: return launch_wgrad_cfg<typename GroupedCfg<DT, CT, true, true, GT_ANY>::T>(p, ga, b, s);
+    case GT_ANY_DEEP: return launch_wgrad_cfg<typename GroupedCfg<DT, CT, true, true, GT_ANY_DEEP>::T>(p, ga, b, s);
+    case GT_64_DEEP: return launch_wgrad_cfg<typename GroupedCfg<DT, CT, true, true, GT_64_DEEP>::T>(p, ga, b, s);
     case GT_64: return launch_wgrad_cfg<typename GroupedCfg<DT, CT, true, true, GT_64>::T>(p, ga, b, s);
     case GT_128: return launch_wgrad_cfg<typename GroupedCfg<DT, CT, true, true, GT_128>::T>(p, ga, b, s);
     case GT_256: return launch_wgrad_cfg<typename GroupedCfg<DT, CT, true, true, GT_256>::T>(p, ga, b, s);
