@@ -171,8 +171,12 @@ int64_t expected_tiles(const GArgs& a, int64_t bm, int64_t bn) {
 }
 
 gemm_grouped_kernel_t pick(const GArgs& a, int cus) {
+  const int64_t rows = (a.M + live_groups(a) - 1) / (live_groups(a) > 0 ? live_groups(a) : 1);
   if (a.wgrad) {
-    if (!tiles_fit(a)) return GEMM_GROUPED_ANY;
+    // Narrow gradients of few rows are all epilogue: the copies through registers take the least LDS,
+    // so that four workgroups share a compute unit (19 groups of 2944 x 64 bf16 from 9 rows 8 us against
+    // 13 on large tiles, 85 of 6168 x 128 fp16 from 14986 rows 157 against 187).
+    if (!tiles_fit(a) || ((a.N < 192 || a.K < 192) && rows <= 256)) return GEMM_GROUPED_ANY;
     auto tiles = [&](int64_t bm, int64_t bn) { return (a.N + bm - 1) / bm * ((a.K + bn - 1) / bn) * a.groups; };
     // large tiles from 5/8 of a round on: 5 groups of 1744 x 1424 (210 tiles) 16 us against 23 on
     // 128 x 128 ones, 4 of 2608 x 704 (132) 18 against 16
@@ -180,14 +184,26 @@ gemm_grouped_kernel_t pick(const GArgs& a, int cus) {
     if (tiles(128, 128) >= cus / 2) return GEMM_GROUPED_MFMA_128;
     return GEMM_GROUPED_MFMA_64;
   }
-  const int64_t rows = (a.M + live_groups(a) - 1) / live_groups(a);
-  // Few rows: what counts is the weights' bytes.  Few 64 x 64 tiles stream too: more waves share out
-  // K (1584 rows over 2 groups, N 80, K 5832, bf16 23 us against 30 on 64 x 64 tiles, 236 x 688 x
-  // 1824 fp16 9 against 13; 545 rows over 6 groups, N 984, K 1432, whose tiles fill most compute
-  // units, 19 against 13).
-  if (stream_fits(a) && (rows <= 64 || 4 * expected_tiles(a, 64, 64) <= cus)) return GEMM_GROUPED_STREAM;
-  if (!tiles_fit(a)) return GEMM_GROUPED_ANY;
-  if (expected_tiles(a, 256, 256) >= cus) return GEMM_GROUPED_MFMA_256;
+  // Few rows a group: what counts is the weights' bytes, and the streaming kernel reads them at the
+  // rate of the memory, but the rows once for every 32 or 64 columns.  How far that carries depends
+  // on whether 128 x 128 tiles, one row of them to a group, would fill the compute units (32 groups of
+  // 2048 x 2048 bf16, B as N x K: 6 rows a group 56 us against 65 on tiles, 16 rows 69 against 65, 32
+  // rows 112 against 72; as K x N 2 rows 46 against 48, 6 rows 54 against 51), or not (one group,
+  // N 8192, K 4096: 32 rows 18 against 21 and 48 rows 23 against 21; as K x N 64 rows 19 against 23), and on
+  // there being tiles for the alignment (without: 16 rows 69 against 71, 32 rows 112 against 105).
+  const bool fits = tiles_fit(a), kn = a.transB == 0, many = live_groups(a) * ((a.N + 127) / 128) >= cus;
+  const int64_t most = fits ? (many ? (kn ? 4 : 8) : (kn ? 64 : 32)) : (kn ? 64 : many ? 24 : 48);
+  // Few 64 x 64 tiles stream too: more waves share out K (1584 rows over 2 groups, N 80, K 5832, bf16
+  // 23 us against 30 on 64 x 64 tiles, 236 x 688 x 1824 fp16 9 against 13; 545 rows over 6 groups, N
+  // 984, K 1432, whose tiles fill most compute units, 19 against 13).
+  if (stream_fits(a) && (rows <= most || 4 * expected_tiles(a, 64, 64) <= cus)) return GEMM_GROUPED_STREAM;
+  // So is a K of at most one and a half K tiles (2439 x 2480 x 160 in 8 bits 15 us against 18 on large
+  // tiles, 207 rows over 16 groups, N 6368, K 96, 13 against 22; 10313 x 2368 x 208 over 7 groups 40
+  // against 30).
+  if (!fits || a.K * (a.i8 ? 1 : 2) <= 192) return GEMM_GROUPED_ANY;
+  // Large tiles, mixed with small ones, from half a round on (1710 x 6576 x 5296 in 8 bits over 3
+  // groups, 234 of them, 76 us against 100 on 128 x 128 tiles; 120 of them 77 against 79, 66 22 against 21).
+  if (2 * expected_tiles(a, 256, 256) >= cus) return GEMM_GROUPED_MFMA_256;
   if (16 * expected_tiles(a, 128, 128) >= 9 * cus) return GEMM_GROUPED_MFMA_128;
   return GEMM_GROUPED_MFMA_64;
 }
