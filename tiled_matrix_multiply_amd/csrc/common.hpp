@@ -59,6 +59,20 @@ constexpr int64_t kSplitSlotBytes = 256 + 256 * 128 * 4;
 // Stream-K workspace slot: one 256 x 256 tile's fp32 partial sums.
 constexpr int64_t kStreamSlotBytes = 256 * 256 * 4;
 
+// The runtime counts the work items of a grid in 32 bits and takes what is beyond them off without
+// an error: more workgroups than that go out in several launches, each (but the last) of whole rounds
+// of the 8 XCDs.  launch(first, n) enqueues the workgroups first .. first + n - 1.
+template <class F>
+inline hipError_t launch_in_slices(int64_t workgroups, int threads, F launch) {
+  const int64_t most = 0xffffffffLL / threads / 8 * 8;
+  for (int64_t first = 0; first < workgroups; first += most) {
+    launch(first, (unsigned)(workgroups - first < most ? workgroups - first : most));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <int DT> struct DTypeInfo;
 template <> struct DTypeInfo<F32> { static constexpr int bytes = 4; };
 template <> struct DTypeInfo<F16> { static constexpr int bytes = 2; };

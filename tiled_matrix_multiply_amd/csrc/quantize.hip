@@ -145,19 +145,25 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const void* X, int64
   for (int64_t c = t + NV * TPR; c < chunks; c += TPR) store(c, fetch(c));
 }
 
+template <int XT, int TPR, int NV>
+hipError_t launch_rows(const void* X, int64_t ldx, int M, int K, int8_t* Q, int64_t ldq, float* scales, hipStream_t s) {
+  constexpr int RPW = 256 / TPR;  // rows of a workgroup
+  return launch_in_slices(((int64_t)M + RPW - 1) / RPW, 256, [&](int64_t first, unsigned n) {
+    const int64_t row = first * RPW;
+    hipLaunchKernelGGL((quantize_rows_kernel<XT, TPR, NV>), dim3(n), dim3(256), 0, s,
+                       reinterpret_cast<const uint8_t*>(X) + row * ldx * QCfg<XT>::ES, ldx, (int)(M - row), K,
+                       Q + row * ldq, ldq, scales + row);
+  });
+}
+
 template <int XT>
 hipError_t launch_type(const void* X, int64_t ldx, int M, int K, int8_t* Q, int64_t ldq, float* scales,
                        hipStream_t s) {
   // A wave holds a row of up to 64 x 4 chunks and needs no barrier; beyond, four waves share one.
   const int64_t chunks = ((int64_t)K + QCfg<XT>::CE - 1) / QCfg<XT>::CE;
-  if (chunks <= 64 * 4)
-    hipLaunchKernelGGL((quantize_rows_kernel<XT, 64, 4>), dim3((unsigned)(((int64_t)M + 3) / 4)), dim3(256), 0, s, X, ldx, M,
-                       K, Q, ldq, scales);
-  else if (chunks <= 256 * 4)
-    hipLaunchKernelGGL((quantize_rows_kernel<XT, 256, 4>), dim3((unsigned)M), dim3(256), 0, s, X, ldx, M, K, Q, ldq, scales);
-  else
-    hipLaunchKernelGGL((quantize_rows_kernel<XT, 256, 8>), dim3((unsigned)M), dim3(256), 0, s, X, ldx, M, K, Q, ldq, scales);
-  return hipGetLastError();
+  if (chunks <= 64 * 4) return launch_rows<XT, 64, 4>(X, ldx, M, K, Q, ldq, scales, s);
+  if (chunks <= 256 * 4) return launch_rows<XT, 256, 4>(X, ldx, M, K, Q, ldq, scales, s);
+  return launch_rows<XT, 256, 8>(X, ldx, M, K, Q, ldq, scales, s);
 }
 
 }  // namespace
