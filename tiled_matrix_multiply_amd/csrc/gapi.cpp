@@ -251,7 +251,7 @@ gemm_status_t run_rows(gemm_handle_t h, gemm_grouped_kernel_t kernel, void* stre
   p.bias = (a.epi & GEMM_EPI_BIAS) ? a.bias : nullptr;
   p.ra = a.sa;
   p.rb = a.sb;
-  const tgemm::GroupArgs ga{a.offsets, (int)a.groups, a.stride_b, 0};
+  const tgemm::GroupArgs ga{a.offsets, (int)a.groups, a.stride_b, 0, 0};
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const bool kn = a.transB == 0;
   tgemm::DeviceGuard g(h->device);
@@ -283,7 +283,7 @@ gemm_status_t run_wgrad(gemm_handle_t h, gemm_grouped_kernel_t kernel, void* str
   if (a.N == 0 || a.groups == 0 || (a.K == 0 && !dbias)) return GEMM_OK;
   if (kernel == GEMM_GROUPED_STREAM) return GEMM_ERR_UNSUPPORTED;
   if ((st = choose(a, h->cu_count, kernel)) != GEMM_OK) return st;
-  const tgemm::GroupArgs ga{a.offsets, (int)a.groups, 0, a.stride_c};
+  const tgemm::GroupArgs ga{a.offsets, (int)a.groups, 0, a.stride_c, 0};
   // The kernels compute C = X^T Y: stored N x K, the gradient is D^T A.
   tgemm::GemmParams p = params(a, alpha, beta, C);
   p.A = a.transB ? a.B : a.A;

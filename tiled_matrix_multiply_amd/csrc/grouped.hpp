@@ -15,7 +15,10 @@ struct GroupArgs {
   int groups;
   int64_t stride_b;        // elements between the groups' B (rows: forward)
   int64_t stride_c;        // elements between the groups' C (weight gradient)
+  int first;               // workgroups before this launch's own (launch_in_slices)
 };
+
+__device__ __forceinline__ int workgroup(const GroupArgs& ga) { return ga.first + (int)blockIdx.x; }
 
 // Upper bound of the row tiles of height bm that any offsets can give M rows.
 inline int64_t max_row_tiles(int64_t M, int64_t groups, int64_t bm) {

@@ -13,7 +13,7 @@ enum GroupedTile : int { GT_ANY = 0, GT_64 = 1, GT_128 = 2, GT_256 = 3, GT_64_DE
 template <class C>
 __global__ __launch_bounds__(C::NT) void grouped_rows_kernel(GemmParams p, GroupArgs ga) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS_BYTES];
-  const GroupItem it = group_item(ga, p.M, C::BM, p.tiles_n, (int)blockIdx.x, threadIdx.x & 63);
+  const GroupItem it = group_item(ga, p.M, C::BM, p.tiles_n, workgroup(ga), threadIdx.x & 63);
   if (it.group < 0) return;
   enter_group<C::ES, DTypeInfo<C::CT>::bytes>(p, ga, it.group, it.row0, it.rows);
   mfma_tile<C>(p, SkSeg{}, smem, tile_pos(it.local, (it.rows + C::BM - 1) / C::BM, p.tiles_n));
@@ -50,7 +50,7 @@ __global__ __launch_bounds__(512) void grouped_rows_mixed_kernel(const GemmParam
   const int tn = (int)(((int64_t)p0.N + 255) >> 8), tn_small = (int)(((int64_t)p0.N + 127) >> 7);
   const int nl = gs.total(large_rows) * tn, ns = gs.total(small_rows) * tn_small;
   const int split = __builtin_amdgcn_readfirstlane(tiles_to_split(nl, ns, cus)), kept = nl - split;
-  const int first_small = (kept + 7) & ~7, bid = (int)blockIdx.x;
+  const int first_small = (kept + 7) & ~7, bid = workgroup(ga);
   if (bid < first_small) {
     const int t = xcd_item(bid, kept);
     if (t < 0) return;
@@ -148,7 +148,7 @@ __device__ __forceinline__ void bias_tile(const BiasGrad& b, const GroupArgs& ga
 template <class C>
 __global__ __launch_bounds__(C::NT) void grouped_wgrad_kernel(GemmParams p, GroupArgs ga, BiasGrad b, int xcd) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS_BYTES];
-  int bid = (int)blockIdx.x;
+  int bid = workgroup(ga);
   if (bid < b.blocks) {
     bias_tile<C::DT, C::NT>(b, ga, p.K, bid);
     return;
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(C::NT) void grouped_wgrad_kernel(GemmParams p, Grou
 }
 
 template <class C>
-hipError_t launch_rows_cfg(GemmParams p, const GroupArgs& ga, hipStream_t s) {
+hipError_t launch_rows_cfg(GemmParams p, GroupArgs ga, hipStream_t s) {
   p.tiles_n = (p.N + C::BN - 1) / C::BN;
   const int64_t grid = whole_rounds(max_row_tiles(p.M, ga.groups, C::BM) * p.tiles_n);
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
@@ -184,12 +184,14 @@ hipError_t launch_rows_cfg(GemmParams p, const GroupArgs& ga, hipStream_t s) {
     if (p.K % C::BKE) p.epi |= FIX_A;
     if (C::B_MN ? p.N % CE : p.K % C::BKE) p.epi |= FIX_B;
   }
-  hipLaunchKernelGGL((grouped_rows_kernel<C>), dim3((unsigned)grid), dim3(C::NT), 0, s, p, ga);
-  return hipGetLastError();
+  return launch_in_slices(grid, C::NT, [&](int64_t first, unsigned n) {
+    ga.first = (int)first;
+    hipLaunchKernelGGL((grouped_rows_kernel<C>), dim3(n), dim3(C::NT), 0, s, p, ga);
+  });
 }
 
 template <class F, class Q>
-hipError_t launch_mixed_cfg(GemmParams p, const GroupArgs& ga, int cus, hipStream_t s) {
+hipError_t launch_mixed_cfg(GemmParams p, GroupArgs ga, int cus, hipStream_t s) {
   const int64_t tn = ((int64_t)p.N + 255) / 256, tn_small = ((int64_t)p.N + 127) / 128;
   int64_t large, small = cus;
   if (ga.offsets) {
@@ -204,17 +206,18 @@ hipError_t launch_mixed_cfg(GemmParams p, const GroupArgs& ga, int cus, hipStrea
   if (small > cus) small = cus;
   const int64_t workers = whole_rounds(small), grid = whole_rounds(large) + workers;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  if (grid == 0) return hipSuccess;
   constexpr int CE = 16 / F::ES;
   static_assert(F::BKE == Q::BKE, "one K tile");
   if (p.K % F::BKE) p.epi |= FIX_A;
   if (F::B_MN ? p.N % CE : p.K % F::BKE) p.epi |= FIX_B;
-  hipLaunchKernelGGL((grouped_rows_mixed_kernel<F, Q>), dim3((unsigned)grid), dim3(512), 0, s, p, ga, cus, (int)workers);
-  return hipGetLastError();
+  return launch_in_slices(grid, 512, [&](int64_t first, unsigned n) {
+    ga.first = (int)first;
+    hipLaunchKernelGGL((grouped_rows_mixed_kernel<F, Q>), dim3(n), dim3(512), 0, s, p, ga, cus, (int)workers);
+  });
 }
 
 template <class C>
-hipError_t launch_wgrad_cfg(GemmParams p, const GroupArgs& ga, BiasGrad b, hipStream_t s) {
+hipError_t launch_wgrad_cfg(GemmParams p, GroupArgs ga, BiasGrad b, hipStream_t s) {
   p.tiles_m = (p.M + C::BM - 1) / C::BM;
   p.tiles_n = (p.N + C::BN - 1) / C::BN;
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
@@ -229,8 +232,10 @@ hipError_t launch_wgrad_cfg(GemmParams p, const GroupArgs& ga, BiasGrad b, hipSt
     if (p.M % CE) p.epi |= FIX_A;
     if (p.N % CE) p.epi |= FIX_B;
   }
-  if (grid > 0) hipLaunchKernelGGL((grouped_wgrad_kernel<C>), dim3((unsigned)grid), dim3(C::NT), 0, s, p, ga, b, xcd);
-  return hipGetLastError();
+  return launch_in_slices(grid, C::NT, [&](int64_t first, unsigned n) {
+    ga.first = (int)first;
+    hipLaunchKernelGGL((grouped_wgrad_kernel<C>), dim3(n), dim3(C::NT), 0, s, p, ga, b, xcd);
+  });
 }
 
 // MfmaCfg of a tile (B_MN / A_MN: stored contiguous along N / M).

@@ -58,7 +58,7 @@ __global__ __launch_bounds__(MF == 1 ? 1024 : 512) void stream_kernel(GemmParams
   extern __shared__ __attribute__((aligned(16))) uint8_t part[];
   const int lane = threadIdx.x & 63, NW = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const GroupItem it = group_item(ga, p.M, C::BM, p.tiles_n, (int)blockIdx.x, lane);
+  const GroupItem it = group_item(ga, p.M, C::BM, p.tiles_n, workgroup(ga), lane);
   if (it.group < 0) return;
   {
     const int ces = c_type == F32 ? 4 : 2;
@@ -294,13 +294,15 @@ __global__ __launch_bounds__(MF == 1 ? 1024 : 512) void stream_kernel(GemmParams
 }
 
 template <int DT, bool KN, int MF>
-hipError_t launch_stream_cfg(GemmParams p, const GroupArgs& ga, int c_type, int waves, hipStream_t s) {
+hipError_t launch_stream_cfg(GemmParams p, GroupArgs ga, int c_type, int waves, hipStream_t s) {
   using C = StreamCfg<DT, KN, MF>;
   p.tiles_n = (p.N + C::BN - 1) / C::BN;
   const int64_t grid = whole_rounds(max_row_tiles(p.M, ga.groups, C::BM) * p.tiles_n);
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((stream_kernel<DT, KN, MF>), dim3((unsigned)grid), dim3(64 * waves), waves * C::PART, s, p, ga, c_type);
-  return hipGetLastError();
+  return launch_in_slices(grid, 64 * waves, [&](int64_t first, unsigned n) {
+    ga.first = (int)first;
+    hipLaunchKernelGGL((stream_kernel<DT, KN, MF>), dim3(n), dim3(64 * waves), waves * C::PART, s, p, ga, c_type);
+  });
 }
 
 // rows: 16, 32 or 64 rows of C per workgroup.
