@@ -47,8 +47,10 @@ typedef enum gemm_grouped_kernel {
  * fp32, groups x N, contiguous (NULL without GEMM_EPI_BIAS).  type: GEMM_F16 or GEMM_BF16, of
  * A, B and C; sums are fp32, rounded once.  Epilogue bits as gemm_run.  With the weights' other
  * transB, and C and A exchanged, the same call is the data gradient dA = dC op(B_g)^T.
- * Errors: as gemm_run (dimensions of at most 2^31 - 1024), plus GEMM_ERR_INVALID_VALUE for groups < 0, stride_b < 0 or NULL offsets
- * with groups > 0, and GEMM_ERR_UNSUPPORTED for groups > 65535 or a kernel whose needs (see
+ * Errors: as gemm_run (dimensions of at most 2^31 - 1024), plus GEMM_ERR_INVALID_VALUE for
+ * groups < 0, stride_b < 0 or NULL offsets with groups > 0, and GEMM_ERR_UNSUPPORTED for groups >
+ * 65535, for about 2^31 tiles of 64 x 64 or more (the most that any offsets can make of M rows; for
+ * the streaming kernel, of 16 x 32, or x 64 for a B stored K x N), or for a kernel whose needs (see
  * gemm_grouped_kernel) do not hold.  M, N or groups of 0 enqueue nothing. */
 GEMM_API gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_grouped_kernel_t kernel,
                                         void* stream, int64_t groups, const int64_t* offsets,
@@ -66,8 +68,9 @@ GEMM_API gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_grouped_kernel_t k
  * C_g starts at C + g * stride_c; the matrices must not overlap.  dbias is fp32, groups x N,
  * contiguous.  type (of A and D): GEMM_F16 or GEMM_BF16; c_type: the same, or GEMM_F32.  Sums are
  * fp32, in an order that depends on the sizes only.  An empty group gives beta * C_g and a zero
- * dbias_g.  Errors: as gemm_run_grouped, with GEMM_ERR_INVALID_VALUE for a stride_c that lets the
- * matrices overlap.  With M = 0 every group is empty. */
+ * dbias_g.  Errors: as gemm_run_grouped (the tiles are those of all groups' gradients), with
+ * GEMM_ERR_INVALID_VALUE for a stride_c that lets the matrices overlap.  With M = 0 every group is
+ * empty. */
 GEMM_API gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, gemm_grouped_kernel_t kernel,
                                               void* stream, int64_t groups,
                                               const int64_t* offsets, int64_t M, int64_t N,

@@ -1,0 +1,90 @@
+"""The host side of the grouped and 8-bit integer calls without a GPU: gapi.cpp under the address and
+undefined-behaviour sanitizers, with launchers that print what they are asked to launch
+(tests/asan/grouped_driver.cpp), and the size checks that the library exports."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+tmm = pytest.importorskip("tiled_matrix_multiply_amd")
+
+F16, BF16, F32 = tmm.GEMM_F16, tmm.GEMM_BF16, tmm.GEMM_F32
+OK, V, U = tmm.GEMM_OK, tmm.GEMM_ERR_INVALID_VALUE, tmm.GEMM_ERR_UNSUPPORTED
+MOST = 2 ** 31 - 1024  # the largest dimension
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    """plan(call, ...): the (status, launch) of each call; a launch is ("tile", number), ("stream",
+    rows, waves) or None."""
+    script = os.path.join(ROOT, "tests", "asan", "grouped.sh")
+    if shutil.which("bash") is None or not os.path.exists("/opt/rocm/llvm/bin/clang"):
+        pytest.skip("no ROCm clang")
+    if not os.path.exists(script):
+        pytest.skip("tests/asan is not in this copy of the tree")
+    exe = str(tmp_path_factory.mktemp("plan") / "driver")
+    r = subprocess.run(["bash", script, exe], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, (r.stdout + r.stderr)[-4000:]
+
+    def run(*calls):
+        r = subprocess.run([exe], input="\n".join(calls), capture_output=True, text=True, timeout=120)
+        assert r.returncode == 0 and "runtime error" not in r.stderr, r.stderr[-4000:]
+        out = []
+        for line in r.stdout.splitlines():
+            w = line.split()
+            launch = {"none": None, "tile": ("tile", int(w[2])) if w[1] == "tile" else None,
+                      "stream": ("stream", int(w[2]), int(w[3])) if w[1] == "stream" else None}[w[1]]
+            out.append((int(w[0]), launch))
+        assert len(out) == len(calls)
+        return out
+
+    return run
+
+
+def call(op, M, N, K, *, groups=1, kernel=0, nk=True, lda=-1, ldb=-1, ldc=-1, stride=-1, skew=0, t=BF16,
+         ct=BF16, dbias=False):
+    return " ".join(str(int(v)) if not isinstance(v, str) else v for v in
+                    (op, kernel, groups, M, N, K, nk, lda, ldb, ldc, stride, skew, t, ct, dbias))
+
+
+# ------------------------------------------------------------------- sizes that cannot be counted --
+
+def far(i):
+    return i << 60
+
+
+def test_checks_refuse_what_the_calls_refuse():
+    """Tiles past 31 bits: the argument checks answer as the calls do."""
+    def products(M, N, groups, i8=0):
+        return tmm.gemm_check_args_grouped(groups, far(1), M, N, 8, 1, far(2), 8, far(5), far(3), 8, 0, far(6),
+                                           far(4), N, i8, BF16, BF16, 0, None)
+
+    def gradient(N, K, groups, dbias=None):
+        return tmm.gemm_check_args_grouped_wgrad(groups, far(1), 40, N, K, 0, far(2), K, far(3), N, far(4), N,
+                                                 N * K, BF16, BF16, dbias)
+
+    for i8 in (0, 1):
+        assert products(2 ** 21, 2 ** 21, 1, i8) == OK
+        assert products(MOST, MOST, 1, i8) == U and products(MOST, MOST, 65535, i8) == U
+        assert products(2 ** 22, 2 ** 20, 1, i8) == OK and products(2 ** 22, 2 ** 21, 1, i8) == U
+        assert products(4096, 2 ** 25, 4096, i8) == U and products(4096, 2 ** 24, 4096, i8) == OK
+    # 2^15 groups of 2^8 x 2^8 tiles are 2^31; a last round of 8 for each row of tiles of a group
+    assert gradient(2 ** 14, 2 ** 14, 2 ** 14) == OK and gradient(2 ** 14, 2 ** 14, 2 ** 15) == U
+    assert gradient(MOST, MOST, 1) == U
+    # the product of the tiles and the groups passes 64 bits
+    for groups in (8192, 2 ** 14, 65535):
+        assert gradient(2 ** 30, 2 ** 30, groups) == U, groups
+
+
+def test_calls_refuse_them(plan):
+    got = plan(call("wgrad", 40, MOST, MOST, groups=65535, nk=False), call("wgrad", 40, MOST, MOST, groups=65535),
+               call("wgrad", 40, 2 ** 30, 2 ** 30, groups=2 ** 14, nk=False),
+               call("grouped", MOST, MOST, 8, groups=65535, stride=0), call("i8", MOST, MOST, 16))
+    assert got == [(U, None)] * 5
+    # too many of the streaming kernel's workgroups, but not of the tiles
+    got = plan(call("grouped", 4096, 2 ** 24 + 8, 96, groups=4096, stride=0),
+               call("grouped", 4096, 2 ** 24 + 8, 96, groups=4096, stride=0, kernel=tmm.GEMM_GROUPED_STREAM),
+               call("grouped", 4096, 2 ** 23, 96, groups=4096, stride=0))
+    assert got[0] == (OK, ("tile", 0)) and got[1] == (U, None) and got[2][1][0] == "stream"

@@ -66,6 +66,18 @@ Range range(const void* p, int64_t rows, int64_t cols, int64_t ld, int size, int
 bool overlaps(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi; }
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// Workgroups must be countable in 31 bits, with the worst case's row tiles and a last round of 8.
+// (Dimensions near 2^31 and many groups pass 63 bits together, hence the 128.)
+bool countable(__int128 row_tiles, int64_t n, int64_t bn) { return row_tiles * ((n + bn - 1) / bn) <= kMaxDim - 16; }
+
+// The same of a whole call, in the smallest tiles that any alignment and size can take: 64 x 64.
+bool countable(const GArgs& a) {
+  if (!a.wgrad) return countable(tgemm::max_row_tiles(a.M, a.groups, 64), a.N, 64);
+  const int64_t rows = a.transB ? a.N : a.K, cols = a.transB ? a.K : a.N;
+  const __int128 tiles = (__int128)((rows + 63) / 64) * ((cols + 63) / 64 + 7);  // a group's, with a last round of 8
+  return countable(((a.N + 63) / 64 + tiles) * a.groups, 1, 1);                  // and its bias gradient's columns
+}
+
 gemm_status_t check(const GArgs& a) {
   if (a.M < 0 || a.N < 0 || a.K < 0 || a.groups < 0) return GEMM_ERR_INVALID_VALUE;
   if (a.transB != 0 && a.transB != 1) return GEMM_ERR_INVALID_VALUE;
@@ -80,6 +92,7 @@ gemm_status_t check(const GArgs& a) {
   if (a.M > kMaxDim || a.N > kMaxDim || a.K > kMaxDim || a.groups > kMaxGroups) return GEMM_ERR_UNSUPPORTED;
   if (a.N == 0 || a.groups == 0) return GEMM_OK;                        // nothing to compute
   if (a.wgrad ? (a.K == 0 && !a.bias) : a.M == 0) return GEMM_OK;
+  if (!countable(a)) return GEMM_ERR_UNSUPPORTED;
   if (!a.offsets && !(a.i8 && a.groups == 1)) return GEMM_ERR_INVALID_VALUE;
   if (!aligned(a.offsets, 8)) return GEMM_ERR_INVALID_VALUE;
   const int in = a.i8 ? 1 : es(a.at), out = es(a.ct);
@@ -154,10 +167,12 @@ bool tiles_fit(const GArgs& a) {
   if (reads && (!rows_ok(a.A, a.lda) || !rows_ok(a.B, a.ldb) || a.stride_b * in % 16 != 0)) return false;
   return aligned(a.C, 16) && a.ldc % 4 == 0 && a.stride_c % 4 == 0;
 }
-// The streaming kernel takes any alignment; stored K x N, four columns at a time.
+// The streaming kernel takes any alignment; stored K x N, four columns at a time.  Its smallest
+// workgroups have 16 rows of 32 (N x K) or 64 columns.
 bool stream_fits(const GArgs& a) {
   const int in = a.i8 ? 1 : es(a.at);
-  return !a.wgrad && (a.transB || a.N >= 4) && a.lda * in <= kMaxRowBytes && a.ldb * in <= kMaxRowBytes;
+  return !a.wgrad && (a.transB || a.N >= 4) && a.lda * in <= kMaxRowBytes && a.ldb * in <= kMaxRowBytes &&
+         countable(tgemm::max_row_tiles(a.M, a.groups, 16), a.N, a.transB ? 32 : 64);
 }
 
 // Groups that can hold rows, and the rows of one on average.
@@ -234,18 +249,12 @@ gemm_status_t choose(const GArgs& a, int cus, gemm_grouped_kernel_t& k) {
   }
 }
 
-// Tiles must be countable in 31 bits, with the worst case's row tiles and a last round of 8.
-bool countable(int64_t row_tiles, int64_t n, int64_t bn) {
-  return (__int128)row_tiles * ((n + bn - 1) / bn) <= kMaxDim - 16;
-}
-
 gemm_status_t run_rows(gemm_handle_t h, gemm_grouped_kernel_t kernel, void* stream, const GArgs& a, float alpha,
                        float beta, void* C) {
   if (!valid(h)) return GEMM_ERR_INVALID_HANDLE;
   gemm_status_t st = check(a);
   if (st != GEMM_OK) return st;
   if (a.M == 0 || a.N == 0 || a.groups == 0) return GEMM_OK;
-  if (!countable(tgemm::max_row_tiles(a.M, a.groups, 64), a.N, 64)) return GEMM_ERR_UNSUPPORTED;
   if ((st = choose(a, h->cu_count, kernel)) != GEMM_OK) return st;
   tgemm::GemmParams p = params(a, alpha, beta, C);
   p.bias = (a.epi & GEMM_EPI_BIAS) ? a.bias : nullptr;
@@ -261,7 +270,6 @@ gemm_status_t run_rows(gemm_handle_t h, gemm_grouped_kernel_t kernel, void* stre
     const int64_t avg = (a.M + live_groups(a) - 1) / live_groups(a);
     int rows = avg <= (a.groups == 1 ? 16 : 10) ? 16 : avg <= (a.groups == 1 ? 32 : 24) ? 32 : 64;
     while (rows > 16 && 4 * expected_tiles(a, rows, kn ? 64 : 32) <= 3 * h->cu_count) rows /= 2;
-    if (!countable(tgemm::max_row_tiles(a.M, a.groups, rows), a.N, kn ? 64 : 32)) return GEMM_ERR_UNSUPPORTED;
     const bool one = expected_tiles(a, rows, kn ? 64 : 32) <= h->cu_count;  // workgroup a compute unit
     const int waves = rows == 64 && kn ? 4 : rows == 16 && one ? 16 : 8;  // (at most 64 KB of LDS)
     return status(a.i8              ? tgemm::launch_stream_i8(p, ga, a.ct, kn, rows, waves, s)
@@ -294,8 +302,6 @@ gemm_status_t run_wgrad(gemm_handle_t h, gemm_grouped_kernel_t kernel, void* str
   p.N = (int)(a.transB ? a.K : a.N);
   p.K = (int)a.M;
   p.epi = 0;
-  const int64_t tiles = ((int64_t)p.M + 63) / 64 * (((int64_t)p.N + 63) / 64 + 7);
-  if (!countable(((a.N + 63) / 64 + tiles) * a.groups, 1, 1)) return GEMM_ERR_UNSUPPORTED;
   const tgemm::BiasGrad b{a.B, a.ldb, (int)a.N, 0, 0, dbias};
   const hipStream_t s = static_cast<hipStream_t>(stream);
   tgemm::DeviceGuard g(h->device);
