@@ -88,3 +88,23 @@ def test_calls_refuse_them(plan):
                call("grouped", 4096, 2 ** 24 + 8, 96, groups=4096, stride=0, kernel=tmm.GEMM_GROUPED_STREAM),
                call("grouped", 4096, 2 ** 23, 96, groups=4096, stride=0))
     assert got[0] == (OK, ("tile", 0)) and got[1] == (U, None) and got[2][1][0] == "stream"
+
+
+# -------------------------------------------------------------------------- leading dimensions --
+
+def test_rows_too_long_for_lane_offsets(plan):
+    """Rows past 2^23 bytes go to the kernel with 64-bit offsets, up to the leading dimensions whose
+    bytes pass 63 bits (which one row alone may have)."""
+    most = 2 ** 23 // 2
+    for lda, launch in ((most, "stream"), (most + 8, "tile"), (2 ** 40, "tile"), (2 ** 62, "tile"), (2 ** 62 + 8, "tile"),
+                        (2 ** 63 - 8, "tile")):
+        st, got = plan(call("grouped", 1, 64, 256, lda=lda))[0]
+        assert st == OK and got[0] == launch, lda
+        if launch == "tile":
+            assert got[1] in (0, 5), lda  # any alignment and length
+    for kernel in (tmm.GEMM_GROUPED_MFMA_64, tmm.GEMM_GROUPED_MFMA_256, tmm.GEMM_GROUPED_STREAM):
+        got = plan(call("grouped", 1, 64, 64, lda=most, kernel=kernel), call("grouped", 1, 64, 64, lda=2 ** 62, kernel=kernel),
+                   call("grouped", 64, 1, 1, nk=False, ldb=2 ** 62, kernel=kernel))
+        assert [st for st, _ in got] == [OK, U, U], kernel
+    got = plan(call("i8", 1, 64, 64, lda=2 ** 23), call("i8", 1, 64, 64, lda=2 ** 23 + 16))
+    assert got[0][1][0] == "stream" and got[1][1] == ("tile", 5)

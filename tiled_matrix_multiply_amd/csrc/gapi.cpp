@@ -156,22 +156,26 @@ bool valid(gemm_handle_t h) { return h && h->magic == tgemm::kHandleMagic; }
 gemm_status_t status(hipError_t e) { return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH; }
 
 constexpr int64_t kMaxRowBytes = int64_t(1) << 23;  // the kernels' 32-bit lane offsets span up to 256 rows
+// (A leading dimension may be any number where there is one row: no product with its size.)
+bool short_rows(int64_t ld, int size) { return ld <= kMaxRowBytes / size; }
+// ld elements are whole 16-byte chunks.
+bool whole_chunks(int64_t ld, int size) { return ld % (16 / size) == 0; }
 
 // The tiled kernels read 16-byte chunks of both operands and store runs of C.
 bool tiles_fit(const GArgs& a) {
   const int in = a.i8 ? 1 : es(a.at);
   auto rows_ok = [&](const void* p, int64_t ld) {
-    return aligned(p, 16) && ld * in % 16 == 0 && ld * in <= kMaxRowBytes;
+    return aligned(p, 16) && whole_chunks(ld, in) && short_rows(ld, in);
   };
   const bool reads = a.wgrad ? a.M > 0 : a.K > 0;
-  if (reads && (!rows_ok(a.A, a.lda) || !rows_ok(a.B, a.ldb) || a.stride_b * in % 16 != 0)) return false;
+  if (reads && (!rows_ok(a.A, a.lda) || !rows_ok(a.B, a.ldb) || !whole_chunks(a.stride_b, in))) return false;
   return aligned(a.C, 16) && a.ldc % 4 == 0 && a.stride_c % 4 == 0;
 }
 // The streaming kernel takes any alignment; stored K x N, four columns at a time.  Its smallest
 // workgroups have 16 rows of 32 (N x K) or 64 columns.
 bool stream_fits(const GArgs& a) {
   const int in = a.i8 ? 1 : es(a.at);
-  return !a.wgrad && (a.transB || a.N >= 4) && a.lda * in <= kMaxRowBytes && a.ldb * in <= kMaxRowBytes &&
+  return !a.wgrad && (a.transB || a.N >= 4) && short_rows(a.lda, in) && short_rows(a.ldb, in) &&
          countable(tgemm::max_row_tiles(a.M, a.groups, 16), a.N, a.transB ? 32 : 64);
 }
 
