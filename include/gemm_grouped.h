@@ -65,12 +65,13 @@ GEMM_API gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_grouped_kernel_t k
  *     dbias_g[n] = sum over the group's rows r of D[r][n]          (NULL: not computed)
  *
  * A is M x K (lda >= K), the forward's input; D is M x N (ldd >= N), the gradient of its output.
- * C_g starts at C + g * stride_c; the matrices must not overlap.  dbias is fp32, groups x N,
- * contiguous.  type (of A and D): GEMM_F16 or GEMM_BF16; c_type: the same, or GEMM_F32.  Sums are
- * fp32, in an order that depends on the sizes only.  An empty group gives beta * C_g and a zero
- * dbias_g.  Errors: as gemm_run_grouped (the tiles are those of all groups' gradients), with
- * GEMM_ERR_INVALID_VALUE for a stride_c that lets the matrices overlap.  With M = 0 every group is
- * empty. */
+ * C_g starts at C + g * stride_c; the matrices follow each other (stride_c of at least a matrix's
+ * extent) or lie side by side (stride_c of at least a row's elements, all groups within ldc).
+ * dbias is fp32, groups x N, contiguous.  type (of A and D): GEMM_F16 or GEMM_BF16; c_type: the
+ * same, or GEMM_F32.  Sums are fp32, in an order that depends on the sizes only.  An empty group
+ * gives beta * C_g and a zero dbias_g.  Errors: as gemm_run_grouped (the tiles are those of all
+ * groups' gradients), with GEMM_ERR_INVALID_VALUE for any other stride_c.  With M = 0 every group
+ * is empty. */
 GEMM_API gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, gemm_grouped_kernel_t kernel,
                                               void* stream, int64_t groups,
                                               const int64_t* offsets, int64_t M, int64_t N,

@@ -101,7 +101,10 @@ gemm_status_t check(const GArgs& a) {
     const int64_t rows = a.transB ? a.N : a.K, cols = a.transB ? a.K : a.N;
     if (a.K > 0) {
       if (!a.C || a.ldc < cols) return GEMM_ERR_INVALID_VALUE;
-      if (a.groups > 1 && (__int128)a.stride_c < (__int128)(rows - 1) * a.ldc + cols) return GEMM_ERR_INVALID_VALUE;
+      // the matrices follow each other, or lie side by side in rows of ldc elements
+      const bool apart = (__int128)a.stride_c >= (__int128)(rows - 1) * a.ldc + cols;
+      const bool beside = a.stride_c >= cols && (__int128)(a.groups - 1) * a.stride_c + cols <= a.ldc;
+      if (a.groups > 1 && !apart && !beside) return GEMM_ERR_INVALID_VALUE;
     }
     if (a.M > 0) {
       if (a.K > 0 && (!a.A || a.lda < a.K)) return GEMM_ERR_INVALID_VALUE;
