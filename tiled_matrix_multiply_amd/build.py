@@ -1,11 +1,11 @@
 """Builds tiled_matrix_multiply_amd/libgemm.so from csrc/ with hipcc for gfx950 only.
 
 Every source is compiled in parallel into _build/, then linked into one shared library whose
-exported symbols are exactly the C ABI of include/gemm.h.
+exported symbols are exactly the C ABI of include/gemm.h and include/gemm_grouped.h.
 
 Beside it, libgemm_lds_poison.so: the same library with the matrix-core kernels of the main
 families (fp32, fp16, bf16, per-tensor and block-scaled E4M3, E2M1 and E2M3, quantized B, and
-the grouped and 8-bit integer products with bf16 results) built with
+the tiles of the grouped and 8-bit integer products) built with
 GEMM_DEBUG_POISON_LDS, which fills every LDS stage with all-ones words before it is refilled.
 It is a race check for the staged K loop: its results must equal libgemm.so's bit for bit.
 """
@@ -24,7 +24,9 @@ LIB = os.path.join(PKG, "libgemm.so")
 LIB_POISON = os.path.join(PKG, "libgemm_lds_poison.so")
 POISON_SOURCES = ("mfma_f32.hip", "mfma_f16.hip", "mfma_bf16.hip", "mfma_e4m3.hip",
                   "mfma_mx_e4m3.hip", "mfma_e2m1.hip", "mfma_e2m3.hip", "qmfma.hip",
-                  "grouped_bf16.hip", "grouped_wgrad_bf16.hip", "grouped_i8_bf16.hip")
+                  "grouped_bf16.hip", "grouped_f16.hip", "grouped_wgrad_bf16.hip",
+                  "grouped_wgrad_f16.hip", "grouped_i8_bf16.hip", "grouped_i8_f16.hip",
+                  "grouped_i8_f32.hip")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
