@@ -108,3 +108,53 @@ def test_rows_too_long_for_lane_offsets(plan):
         assert [st for st, _ in got] == [OK, U, U], kernel
     got = plan(call("i8", 1, 64, 64, lda=2 ** 23), call("i8", 1, 64, 64, lda=2 ** 23 + 16))
     assert got[0][1][0] == "stream" and got[1][1] == ("tile", 5)
+
+
+# ---------------------------------------------------------------------------- the kernel choice --
+
+def tile(n):
+    return ("tile", n)
+
+
+# what AUTO takes on both sides of each border of its rule, with 256 compute units; tiles: 0 any alignment
+# (5 with K split), 1 64 x 64 (4 with more stages), 2 128 x 128, 3 256 x 256
+@pytest.mark.parametrize("args,launch", [
+    # few rows a group: 8 and 4 where 128 x 128 tiles would fill the compute units ...
+    (("grouped", 256, 2048, 2048, dict(groups=32)), "stream"), (("grouped", 288, 2048, 2048, dict(groups=32)), tile(3)),
+    (("grouped", 128, 2048, 2048, dict(groups=32, nk=False)), "stream"),
+    (("grouped", 160, 2048, 2048, dict(groups=32, nk=False)), tile(3)),
+    # ... 32 and 64 where not, 24 or 48 (64) without tiles for the alignment
+    (("grouped", 32, 8192, 4096, dict()), "stream"), (("grouped", 33, 8192, 4096, dict()), tile(4)),
+    (("grouped", 64, 8192, 4096, dict(nk=False)), "stream"), (("grouped", 65, 8192, 4096, dict(nk=False)), tile(4)),
+    (("grouped", 48, 8192, 4096, dict(skew=2)), "stream"), (("grouped", 49, 8192, 4096, dict(skew=2)), tile(5)),
+    (("grouped", 768, 2048, 2048, dict(groups=32, skew=2)), "stream"),
+    (("grouped", 800, 2048, 2048, dict(groups=32, skew=2)), tile(0)),
+    # at most a quarter of the compute units in 64 x 64 tiles
+    (("grouped", 512, 512, 1824, dict()), "stream"), (("grouped", 512, 576, 1824, dict()), tile(4)),
+    # a K of one and a half K tiles
+    (("grouped", 8192, 8192, 96, dict()), tile(0)), (("grouped", 8192, 8192, 104, dict()), tile(3)),
+    (("i8", 8192, 8192, 192, dict()), tile(0)), (("i8", 8192, 8192, 208, dict()), tile(3)),
+    # half a round of 256 x 256 tiles, 9/16 of one of 128 x 128
+    (("grouped", 2048, 4096, 2048, dict()), tile(3)), (("grouped", 2048, 3840, 2048, dict()), tile(2)),
+    (("grouped", 1536, 1536, 2048, dict()), tile(2)), (("grouped", 1536, 1408, 2048, dict()), tile(1)),
+    # 64 x 64: more stages up to one tile a compute unit
+    (("grouped", 1024, 1024, 2048, dict()), tile(4)), (("grouped", 1024, 1088, 2048, dict()), tile(1)),
+    # gradients: large tiles from 5/8 of a round, 128 x 128 from half of one
+    (("wgrad", 4096, 2560, 4096, dict()), tile(3)), (("wgrad", 4096, 2304, 4096, dict()), tile(2)),
+    (("wgrad", 4096, 1024, 2048, dict()), tile(2)), (("wgrad", 4096, 1024, 1920, dict()), tile(1)),
+    (("wgrad", 4096, 1024, 1024, dict()), tile(4)), (("wgrad", 4096, 1024, 1088, dict()), tile(1)),
+    # ... narrow ones of few rows, and those without tiles for the alignment
+    (("wgrad", 256, 2048, 184, dict()), tile(5)), (("wgrad", 257, 2048, 184, dict()), tile(4)),
+    (("wgrad", 256, 2048, 192, dict()), tile(4)), (("wgrad", 4096, 2560, 4096, dict(skew=2)), tile(0)),
+    # the sizes of test_gpu_grouped_paths.py
+    (("grouped", 3977, 2568, 104, dict(groups=6)), tile(3)), (("grouped_i8", 4451, 4112, 208, dict(groups=15)), tile(3)),
+    (("i8", 4100, 4112, 208, dict()), tile(3)), (("grouped", 1314, 1001, 75, dict(groups=3, lda=78, skew=2)), tile(0)),
+    (("grouped", 19003, 5, 203, dict(groups=3, lda=206, skew=2)), tile(0)),
+    (("grouped", 64, 16385, 203, dict(nk=False, skew=2)), ("stream", 64)),
+    (("grouped", 1000, 1003, 203, dict(nk=False, skew=2, kernel=5)), ("stream", 64)),
+])
+def test_auto(plan, args, launch):
+    op, M, N, K, kw = args
+    st, got = plan(call(op, M, N, K, **kw))[0]
+    assert st == OK
+    assert got[0] == launch if isinstance(launch, str) else got[:len(launch)] == launch
