@@ -27,7 +27,7 @@ __global__ __launch_bounds__(C::NT) void grouped_rows_kernel(GemmParams p, Group
 // the time of the last rounds is estimated both ways in tenths of a large tile, small ones filling
 // the holes of a started round two to a hole.  Large tiles come first, so that the small ones end
 // the launch.  Measured (4096 rows over 8 groups, N 4096, K 2048, bf16; 8190 over 16, N 2048, K
-// 4096, fp16): 115 and 222 us with large tiles alone, 87 and 171 mixed.
+// 4096, fp16): 115 and 222 us with large tiles alone, 86 to 88 and 161 to 171 mixed.
 __host__ __device__ __forceinline__ int large_rows(int rows) { return (int)(((int64_t)rows + 127) >> 8); }
 __host__ __device__ __forceinline__ int small_rows(int rows) { return (rows & 255) && (rows & 255) <= 128 ? 1 : 0; }
 // How many of nl large tiles to split, beside ns small ones.
@@ -144,7 +144,9 @@ __device__ __forceinline__ void bias_tile(const BiasGrad& b, const GroupArgs& ga
 // (8 groups of 4096 x 2048 bf16 from 4096 uneven rows: 90 us in their own order, 84 so).
 // What bounds it with few rows to a group is the writing of the gradient, which the products do not
 // hide: those 8 groups take 30 us with no rows at all and 0.1 us more for each row of a group (53 us
-// for 512, 1.3 PFLOP/s).  16 groups of 4096 x 2048 from 16383 rows in fp32: 320 us, 0.5 GB written.
+// for 512, 1.3 PFLOP/s).  16 groups of 4096 x 2048 from 16383 rows in fp32: 315 to 326 us, 0.5 GB
+// written.  With beta C is read as the sums are laid out, 16 bytes of each of 32 rows an instruction,
+// and nothing hides it: these two take 132 and 418 us.
 template <class C>
 __global__ __launch_bounds__(C::NT) void grouped_wgrad_kernel(GemmParams p, GroupArgs ga, BiasGrad b, int xcd) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS_BYTES];

@@ -10,7 +10,9 @@
 //    fragment stand for and transposes them with byte permutes: 64 columns, NF = 4 fragments
 //    (column 4 i + j of the block is row i of fragment j).
 // What bounds it is the weights' bytes: 1 x 28672 x 8192 in 8 bits 46 us (5.1 TB/s), 32 rows over 64
-// groups (23 of them with rows) of 1024 x 2048 19 us in bf16 (5.1 TB/s) and 11 us in 8 bits (4.4).
+// groups (23 of them with rows) of 1024 x 2048 19 us in bf16 (5.0 to 5.2 TB/s) and 11 us in 8 bits
+// (4.5).  More than 64 groups cost each workgroup a walk over the offsets: 64 rows, one to a group, over
+// 64, 128 and 256 groups 52, 51 and 55 us in bf16 and 31, 34 and 37 in 8 bits.
 // With few columns it is the loads of a compute unit: 37 x 4104 x 4112 in 8 bits, stored K x N in
 // 4-byte pieces, 12 us (1.4 TB/s).
 // Any alignment and size: loads are unaligned, columns past N repeat the last ones and are not

@@ -1041,7 +1041,7 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, ui
     __syncthreads();  // outside the condition: the groups of a split K loop count tiles apart
 #endif
     if (kt + C::S < KT) {  // into the buffers tile kt has released
-            if constexpr (DEFER_B) issue_a(tile_of(kt + C::S), abuf);
+      if constexpr (DEFER_B) issue_a(tile_of(kt + C::S), abuf);
       else issue(kt + C::S, abuf);
     }
   };
@@ -1424,7 +1424,9 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, ui
   const int nw = n0 + wn * C::WTN + lhalf * 4;
   {
     // 8-bit integers: the sums become fp32 in place, scaled by alpha times their row's scale, then
-    // by their column's; the rest of the epilogue is the other types'.
+    // by their column's; the rest of the epilogue is the other types'.  On the mixed kernel of the
+    // grouped products this part spills 10 vector registers (44 bytes a lane) with bf16 and fp32
+    // results and 2 with fp16 ones, as the fp16 products' does; none inside the K loop.
     constexpr bool INT = C::DT == I8;
     auto val = [&](int i, int j, int r) {
       if constexpr (INT) return __int_as_float(acc[i][j][r]);
