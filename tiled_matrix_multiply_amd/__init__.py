@@ -75,6 +75,18 @@ GROUPED_EXPORTS = ("gemm_run_grouped", "gemm_run_grouped_wgrad", "gemm_run_i8",
                    "gemm_run_grouped_i8", "gemm_quantize_rows", "gemm_check_args_grouped",
                    "gemm_check_args_grouped_wgrad", "gemm_check_args_quantize_rows")
 
+# gemm_score_t
+GEMM_SCORE_SOFTMAX, GEMM_SCORE_SIGMOID = 0, 1
+SCORE = {"softmax": GEMM_SCORE_SOFTMAX, "sigmoid": GEMM_SCORE_SIGMOID}
+
+# Every symbol include/gemm_experts.h declares.
+EXPERTS_EXPORTS = ("gemm_route_workspace_bytes", "gemm_route", "gemm_route_grad", "gemm_dispatch_rows",
+                   "gemm_combine_rows", "gemm_combine_rows_grad", "gemm_quantize_mx",
+                   "gemm_run_grouped_mx", "gemm_check_args_route", "gemm_check_args_route_grad",
+                   "gemm_check_args_dispatch_rows", "gemm_check_args_combine_rows",
+                   "gemm_check_args_combine_rows_grad", "gemm_check_args_quantize_mx",
+                   "gemm_check_args_grouped_mx")
+
 # libgemm.so must resolve its libamdhip64.so.7 dependency to the HIP runtime instance that owns
 # the caller's device pointers and streams.  PyTorch ships its own runtime (soname
 # libamdhip64.so.7, but its libraries ask for plain "libamdhip64.so"): if libgemm.so were loaded
@@ -176,6 +188,30 @@ _lib.gemm_check_args_grouped_wgrad.argtypes = _GRP + [_vp, _i64, _vp, _i64, _vp,
 _lib.gemm_check_args_grouped_wgrad.restype = _int
 _lib.gemm_check_args_quantize_rows.argtypes = [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp]
 _lib.gemm_check_args_quantize_rows.restype = _int
+_lib.gemm_route_workspace_bytes.argtypes = [_i64, _i64]
+_lib.gemm_route_workspace_bytes.restype = _i64
+_RT = [_i64, _i64, _i64, _vp, _i64, _int, _int]  # tokens, experts, top, logits, ldl, x_type, score
+_lib.gemm_route.argtypes = [_vp, _vp] + _RT + [_vp, _i64, _i64, _int, _int, _f32, _vp, _vp, _vp, _vp, _vp,
+                                               _i64]
+_lib.gemm_check_args_route.argtypes = _RT + [_vp, _i64, _i64, _int, _int, _vp, _vp, _vp, _vp, _vp, _i64]
+_lib.gemm_route_grad.argtypes = [_vp, _vp] + _RT + [_int, _f32, _vp, _vp, _vp, _i64]
+_lib.gemm_check_args_route_grad.argtypes = _RT + [_int, _vp, _vp, _vp, _i64]
+_MV = [_i64, _i64, _i64, _vp, _i64]  # tokens, top, K, X, ldx
+_lib.gemm_check_args_dispatch_rows.argtypes = _MV + [_int, _vp, _i64, _vp, _i64]
+_lib.gemm_dispatch_rows.argtypes = [_vp, _vp] + _lib.gemm_check_args_dispatch_rows.argtypes
+_lib.gemm_check_args_combine_rows.argtypes = _MV + [_int, _vp, _i64, _vp, _vp, _i64]
+_lib.gemm_combine_rows.argtypes = [_vp, _vp] + _MV + [_int, _vp, _i64, _vp, _f32, _vp, _i64]
+_lib.gemm_check_args_combine_rows_grad.argtypes = _MV + [_vp, _i64, _int, _vp, _i64, _vp, _vp, _i64, _vp]
+_lib.gemm_combine_rows_grad.argtypes = [_vp, _vp] + _lib.gemm_check_args_combine_rows_grad.argtypes
+_lib.gemm_check_args_quantize_mx.argtypes = [_i64, _i64, _vp, _i64, _int, _i64, _vp, _i64, _vp, _i64, _int,
+                                             _vp, _i64]
+_lib.gemm_quantize_mx.argtypes = [_vp, _vp] + _lib.gemm_check_args_quantize_mx.argtypes
+_GMX = [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64]  # A, lda, sa, ldsa, B .. stride_sb
+_lib.gemm_run_grouped_mx.argtypes = [_vp, _int, _vp] + _GRP[:5] + [_f32] + _GMX + [_f32, _vp, _i64, _int, _int,
+                                                                                   _u32, _vp]
+_lib.gemm_check_args_grouped_mx.argtypes = _GRP[:5] + _GMX + [_vp, _i64, _int, _int, _u32, _vp]
+for _name in EXPERTS_EXPORTS[1:]:
+    getattr(_lib, _name).restype = _int
 _lib.gemm_status_string.argtypes = [_int]
 _lib.gemm_status_string.restype = ctypes.c_char_p
 
@@ -400,6 +436,98 @@ def gemm_check_args_quantize_rows(M, K, X, ldx, x_type, Q, ldq, scales) -> int:
     return _lib.gemm_check_args_quantize_rows(M, K, X, ldx, x_type, Q, ldq, scales)
 
 
+def gemm_route_workspace_bytes(tokens, experts) -> int:
+    """Workspace bytes gemm_route needs, or a negative status."""
+    return _lib.gemm_route_workspace_bytes(tokens, experts)
+
+
+def gemm_route(handle, stream, tokens, experts, top, logits, ldl, x_type, score, bias, groups, top_groups,
+               group_top, renorm, scale, expert, weight, place, offsets, workspace, workspace_bytes) -> int:
+    """Raw router (include/gemm_experts.h): returns the status code (no exception)."""
+    return _lib.gemm_route(handle, stream, tokens, experts, top, logits, ldl, x_type, score, bias, groups,
+                           top_groups, group_top, renorm, scale, expert, weight, place, offsets, workspace,
+                           workspace_bytes)
+
+
+def gemm_route_grad(handle, stream, tokens, experts, top, logits, ldl, x_type, score, renorm, scale, expert,
+                    dweight, dlogits, ldd) -> int:
+    """Raw gradient of the router's logits: returns the status code (no exception)."""
+    return _lib.gemm_route_grad(handle, stream, tokens, experts, top, logits, ldl, x_type, score, renorm,
+                                scale, expert, dweight, dlogits, ldd)
+
+
+def gemm_dispatch_rows(handle, stream, tokens, top, K, X, ldx, dtype, place, rows, A, lda) -> int:
+    """Raw dispatch of rows: returns the status code (no exception)."""
+    return _lib.gemm_dispatch_rows(handle, stream, tokens, top, K, X, ldx, dtype, place, rows, A, lda)
+
+
+def gemm_combine_rows(handle, stream, tokens, top, K, Y, ldy, dtype, place, rows, weight, beta, C,
+                      ldc) -> int:
+    """Raw combination of rows: returns the status code (no exception)."""
+    return _lib.gemm_combine_rows(handle, stream, tokens, top, K, Y, ldy, dtype, place, rows, weight, beta, C,
+                                  ldc)
+
+
+def gemm_combine_rows_grad(handle, stream, tokens, top, K, D, ldd, Y, ldy, dtype, place, rows, weight, dY,
+                           lddy, dweight) -> int:
+    """Raw gradients of the combination: returns the status code (no exception)."""
+    return _lib.gemm_combine_rows_grad(handle, stream, tokens, top, K, D, ldd, Y, ldy, dtype, place, rows,
+                                       weight, dY, lddy, dweight)
+
+
+def gemm_quantize_mx(handle, stream, M, K, X, ldx, x_type, top, place, rows, Q, ldq, q_type, S, lds) -> int:
+    """Raw quantization of rows to MXFP4: returns the status code (no exception)."""
+    return _lib.gemm_quantize_mx(handle, stream, M, K, X, ldx, x_type, top, place, rows, Q, ldq, q_type, S,
+                                 lds)
+
+
+def gemm_run_grouped_mx(handle, kernel, stream, groups, offsets, M, N, K, alpha, A, lda, sa, ldsa, B, ldb,
+                        stride_b, sb, ldsb, stride_sb, beta, C, ldc, dtype, c_type, epilogue, bias) -> int:
+    """Raw grouped product in MXFP4: returns the status code (no exception)."""
+    return _lib.gemm_run_grouped_mx(handle, kernel, stream, groups, offsets, M, N, K, alpha, A, lda, sa, ldsa,
+                                    B, ldb, stride_b, sb, ldsb, stride_sb, beta, C, ldc, dtype, c_type,
+                                    epilogue, bias)
+
+
+def gemm_check_args_route(tokens, experts, top, logits, ldl, x_type, score, bias, groups, top_groups,
+                          group_top, renorm, expert, weight, place, offsets, workspace,
+                          workspace_bytes) -> int:
+    """Pointers are integers (device addresses) or None.  Returns the status code."""
+    return _lib.gemm_check_args_route(tokens, experts, top, logits, ldl, x_type, score, bias, groups,
+                                      top_groups, group_top, renorm, expert, weight, place, offsets,
+                                      workspace, workspace_bytes)
+
+
+def gemm_check_args_route_grad(tokens, experts, top, logits, ldl, x_type, score, renorm, expert, dweight,
+                               dlogits, ldd) -> int:
+    return _lib.gemm_check_args_route_grad(tokens, experts, top, logits, ldl, x_type, score, renorm, expert,
+                                           dweight, dlogits, ldd)
+
+
+def gemm_check_args_dispatch_rows(tokens, top, K, X, ldx, dtype, place, rows, A, lda) -> int:
+    return _lib.gemm_check_args_dispatch_rows(tokens, top, K, X, ldx, dtype, place, rows, A, lda)
+
+
+def gemm_check_args_combine_rows(tokens, top, K, Y, ldy, dtype, place, rows, weight, C, ldc) -> int:
+    return _lib.gemm_check_args_combine_rows(tokens, top, K, Y, ldy, dtype, place, rows, weight, C, ldc)
+
+
+def gemm_check_args_combine_rows_grad(tokens, top, K, D, ldd, Y, ldy, dtype, place, rows, weight, dY, lddy,
+                                      dweight) -> int:
+    return _lib.gemm_check_args_combine_rows_grad(tokens, top, K, D, ldd, Y, ldy, dtype, place, rows, weight,
+                                                  dY, lddy, dweight)
+
+
+def gemm_check_args_quantize_mx(M, K, X, ldx, x_type, top, place, rows, Q, ldq, q_type, S, lds) -> int:
+    return _lib.gemm_check_args_quantize_mx(M, K, X, ldx, x_type, top, place, rows, Q, ldq, q_type, S, lds)
+
+
+def gemm_check_args_grouped_mx(groups, offsets, M, N, K, A, lda, sa, ldsa, B, ldb, stride_b, sb, ldsb,
+                               stride_sb, C, ldc, dtype, c_type, epilogue, bias) -> int:
+    return _lib.gemm_check_args_grouped_mx(groups, offsets, M, N, K, A, lda, sa, ldsa, B, ldb, stride_b, sb,
+                                           ldsb, stride_sb, C, ldc, dtype, c_type, epilogue, bias)
+
+
 # ----------------------------------------------------------------- tensor helpers --
 
 _current_stream = None
@@ -596,6 +724,108 @@ def quantize_rows(handle, X, Q, scales, *, M, K, x_type="bf16", ldx=None, ldq=No
         raise GemmError(st, "gemm_quantize_rows")
 
 
+def route_workspace_bytes(tokens: int, experts: int) -> int:
+    """Bytes of the workspace that `route` needs (0 for up to 64 tokens).  Raises GemmError for sizes it
+    refuses."""
+    n = gemm_route_workspace_bytes(tokens, experts)
+    if n < 0:
+        raise GemmError(n, "gemm_route_workspace_bytes")
+    return n
+
+
+def route(handle, logits, expert, weight, place, offsets, *, tokens, experts, top, x_type="f32",
+          score="softmax", bias=None, groups=1, top_groups=1, group_top=1, renorm=False, scale=1.0, ldl=None,
+          workspace=None, workspace_bytes=None, stream=None):
+    """The `top` experts of each token, their weights, and the rows' order by expert, on device tensors:
+    expert and place int32 and weight fp32, tokens x top; offsets int64, experts + 1 (the groups of
+    run_grouped).  workspace: a tensor of route_workspace_bytes(tokens, experts) bytes (None where that
+    is 0).  Raises GemmError on a negative status."""
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.nbytes
+    st = _lib.gemm_route(handle, _stream(stream), tokens, experts, top, _ptr(logits),
+                         ldl if ldl is not None else experts, DTYPE[x_type], SCORE[score], _ptr(bias), groups,
+                         top_groups, int(group_top), int(renorm), float(scale), _ptr(expert), _ptr(weight),
+                         _ptr(place), _ptr(offsets), _ptr(workspace), workspace_bytes)
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_route")
+
+
+def route_grad(handle, logits, expert, dweight, dlogits, *, tokens, experts, top, x_type="f32",
+               score="softmax", renorm=False, scale=1.0, ldl=None, ldd=None, stream=None):
+    """The gradient of route's logits (tokens x experts, every element written) from that of its weights.
+    Raises GemmError on a negative status."""
+    st = _lib.gemm_route_grad(handle, _stream(stream), tokens, experts, top, _ptr(logits),
+                              ldl if ldl is not None else experts, DTYPE[x_type], SCORE[score], int(renorm),
+                              float(scale), _ptr(expert), _ptr(dweight), _ptr(dlogits),
+                              ldd if ldd is not None else experts)
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_route_grad")
+
+
+def dispatch_rows(handle, X, place, A, *, tokens, top, K, rows, dtype="bf16", ldx=None, lda=None, stream=None):
+    """A[place[t][j]] = X[t] for the rows X of the tokens (A: rows x K).  Raises GemmError on a negative
+    status."""
+    st = _lib.gemm_dispatch_rows(handle, _stream(stream), tokens, top, K, _ptr(X), ldx if ldx is not None else K,
+                                 DTYPE[dtype], _ptr(place), rows, _ptr(A), lda if lda is not None else K)
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_dispatch_rows")
+
+
+def combine_rows(handle, Y, place, C, *, tokens, top, K, rows, weight=None, dtype="bf16", beta=0.0, ldy=None,
+                 ldc=None, stream=None):
+    """C[t] = sum over j of weight[t][j] Y[place[t][j]] + beta C[t] (weight None: 1; Y: rows x K).  Raises
+    GemmError on a negative status."""
+    st = _lib.gemm_combine_rows(handle, _stream(stream), tokens, top, K, _ptr(Y), ldy if ldy is not None else K,
+                                DTYPE[dtype], _ptr(place), rows, _ptr(weight), float(beta), _ptr(C),
+                                ldc if ldc is not None else K)
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_combine_rows")
+
+
+def combine_rows_grad(handle, D, Y, place, weight, dY, dweight, *, tokens, top, K, rows, dtype="bf16", ldd=None,
+                      ldy=None, lddy=None, stream=None):
+    """The gradients of combine_rows from D, that of C: dY[place[t][j]] = weight[t][j] D[t] and dweight[t][j]
+    = D[t] . Y[place[t][j]].  Raises GemmError on a negative status."""
+    st = _lib.gemm_combine_rows_grad(handle, _stream(stream), tokens, top, K, _ptr(D),
+                                     ldd if ldd is not None else K, _ptr(Y), ldy if ldy is not None else K,
+                                     DTYPE[dtype], _ptr(place), rows, _ptr(weight), _ptr(dY),
+                                     lddy if lddy is not None else K, _ptr(dweight))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_combine_rows_grad")
+
+
+def quantize_mx(handle, X, Q, S, *, M, K, x_type="bf16", place=None, top=1, rows=None, q_type="e2m1", ldx=None,
+                ldq=None, lds=None, stream=None):
+    """Rows in MXFP4: Q holds two elements a byte, S a scale byte for 32 of them (lds bytes a row); with
+    place row i goes to the rows place[i][j], as dispatch_rows would send it.  Raises GemmError on a
+    negative status."""
+    st = _lib.gemm_quantize_mx(handle, _stream(stream), M, K, _ptr(X), ldx if ldx is not None else K,
+                               DTYPE[x_type], top, _ptr(place), rows if rows is not None else M, _ptr(Q),
+                               ldq if ldq is not None else K, DTYPE[q_type], _ptr(S),
+                               lds if lds is not None else K // 32)
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_quantize_mx")
+
+
+def run_grouped_mx(handle, A, sa, B, sb, C, offsets, *, groups, M, N, K, a_type="e2m1", c_type="bf16", alpha=1.0,
+                   beta=0.0, epilogue=GEMM_EPI_NONE, bias=None, lda=None, ldsa=None, ldb=None, ldsb=None,
+                   stride_b=None, stride_sb=None, ldc=None, kernel=GEMM_GROUPED_AUTO, stream=None):
+    """C[r] = epi(alpha A[r] B_g^T + beta C[r] + bias_g) for the rows r of each group g, with A (M x K) and
+    B_g (N x K) in MXFP4: packed elements, and scale bytes sa and sb (ldsa and ldsb bytes a row).
+    offsets None: one group has all rows.  Raises GemmError on a negative status."""
+    ldb = ldb if ldb is not None else K
+    ldsb = ldsb if ldsb is not None else K // 32
+    st = _lib.gemm_run_grouped_mx(handle, int(kernel), _stream(stream), groups, _ptr(offsets), M, N, K,
+                                  float(alpha), _ptr(A), lda if lda is not None else K, _ptr(sa),
+                                  ldsa if ldsa is not None else K // 32, _ptr(B), ldb,
+                                  stride_b if stride_b is not None else N * ldb, _ptr(sb), ldsb,
+                                  stride_sb if stride_sb is not None else N * ldsb, float(beta), _ptr(C),
+                                  ldc if ldc is not None else N, DTYPE[a_type], DTYPE[c_type], int(epilogue),
+                                  _ptr(bias))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_run_grouped_mx")
+
+
 class Gemm:
     """Owns one handle (gemm_create / gemm_destroy)."""
 
@@ -641,3 +871,10 @@ class Gemm:
     run_i8 = run_i8
     run_grouped_i8 = run_grouped_i8
     quantize_rows = quantize_rows
+    route = route
+    route_grad = route_grad
+    dispatch_rows = dispatch_rows
+    combine_rows = combine_rows
+    combine_rows_grad = combine_rows_grad
+    quantize_mx = quantize_mx
+    run_grouped_mx = run_grouped_mx

@@ -1,0 +1,76 @@
+// Arguments of the kernels behind include/gemm_experts.h (gfx950 only).
+#pragma once
+
+#include "common.hpp"
+
+namespace tgemm {
+
+struct RouteArgs {
+  const void* x;  // logits
+  int64_t ldx;
+  int T, E, top;
+  int x_type, score;  // DType; 0 softmax, 1 sigmoid
+  const float* bias;
+  int groups, top_groups, group_top;
+  int renorm;
+  float scale;
+  int32_t* expert;
+  float* weight;
+  int32_t* place;
+  int64_t* offsets;
+  uint8_t* ws;  // tokens of each expert in each block, route_row_bytes(E) bytes a block; null: one block
+};
+
+struct RouteGradArgs {
+  const void* x;
+  int64_t ldx;
+  int T, E, top;
+  int x_type, score, renorm;
+  float scale;
+  const int32_t* expert;
+  const float* dw;
+  void* dx;
+  int64_t ldd;
+};
+
+// Tokens of one workgroup of the router, at most 64: a token is a bit of a 64-bit mask there.
+inline int route_block_tokens(int64_t T) { return T <= 64 ? 64 : T <= 16384 ? 16 : T <= 32768 ? 32 : 64; }
+inline int64_t route_blocks(int64_t T) { return (T + route_block_tokens(T) - 1) / route_block_tokens(T); }
+constexpr __host__ __device__ int64_t route_row_bytes(int64_t E) { return (E + 15) / 16 * 16; }
+
+struct RowArgs {
+  const void* X;  // dispatch: tokens; combine: the experts' rows
+  int64_t ldx;
+  int T, top, K, R;
+  const int32_t* place;
+  const float* weight;  // null: 1
+  float beta;
+  void* Y;
+  int64_t ldy;
+};
+
+struct RowGradArgs {
+  const void* D;
+  int64_t ldd;
+  const void* Y;
+  int64_t ldy;
+  int T, top, K, R;
+  const int32_t* place;
+  const float* weight;
+  void* dY;
+  int64_t lddy;
+  float* dw;
+};
+
+struct QuantizeMxArgs {
+  const void* X;
+  int64_t ldx;
+  int M, K, top, R;
+  const int32_t* place;  // null: row i to row i
+  uint8_t* Q;
+  int64_t ldq;  // bytes
+  uint8_t* S;
+  int64_t lds;
+};
+
+}  // namespace tgemm

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "checks.hpp"
 #include "grouped.hpp"
 #include "handle.hpp"
 
@@ -28,7 +29,8 @@ hipError_t launch_quantize_rows(const void* X, int64_t ldx, int M, int K, int x_
 
 namespace {
 
-constexpr int64_t kMaxDim = 0x7fffffff - 1023;  // tile edges past a dimension still fit 31 bits
+using namespace tgemm::checks;
+
 constexpr int64_t kMaxGroups = 65535;
 constexpr int64_t kMaxK8 = 131071;  // 128 * 128 * K < 2^31
 
@@ -51,20 +53,6 @@ struct GArgs {
   uint32_t epi;
   const float* bias;  // read; for the gradient dbias, written
 };
-
-int es(gemm_dtype_t t) { return t == GEMM_F32 ? 4 : t == GEMM_F16 || t == GEMM_BF16 ? 2 : 0; }
-
-struct Range {
-  __int128 lo, hi;
-};
-// Byte range of `count` matrices of rows x cols elements of `size` bytes, `stride` elements apart.
-Range range(const void* p, int64_t rows, int64_t cols, int64_t ld, int size, int64_t count = 1, int64_t stride = 0) {
-  const __int128 lo = (__int128)(uintptr_t)p;
-  if (!p || rows <= 0 || cols <= 0 || count <= 0) return {lo, lo};
-  return {lo, lo + ((__int128)(count - 1) * stride + (__int128)(rows - 1) * ld + cols) * size};
-}
-bool overlaps(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi; }
-bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // Workgroups must be countable in 31 bits, with the worst case's row tiles and a last round of 8.
 // (Dimensions near 2^31 and many groups pass 63 bits together, hence the 128.)
@@ -154,11 +142,6 @@ tgemm::GemmParams params(const GArgs& a, float alpha, float beta, void* C) {
   return p;
 }
 
-bool valid(gemm_handle_t h) { return h && h->magic == tgemm::kHandleMagic; }
-
-gemm_status_t status(hipError_t e) { return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH; }
-
-constexpr int64_t kMaxRowBytes = int64_t(1) << 23;  // the kernels' 32-bit lane offsets span up to 256 rows
 // (A leading dimension may be any number where there is one row: no product with its size.)
 bool short_rows(int64_t ld, int size) { return ld <= kMaxRowBytes / size; }
 // ld elements are whole 16-byte chunks.

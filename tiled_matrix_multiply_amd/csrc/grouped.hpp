@@ -16,6 +16,7 @@ struct GroupArgs {
   int64_t stride_b;        // elements between the groups' B (rows: forward)
   int64_t stride_c;        // elements between the groups' C (weight gradient)
   int first;               // workgroups before this launch's own (launch_in_slices)
+  int64_t stride_sb;       // bytes between the groups' block scales of B (microscaled products)
 };
 
 __device__ __forceinline__ int workgroup(const GroupArgs& ga) { return ga.first + (int)blockIdx.x; }
@@ -154,8 +155,8 @@ __device__ __forceinline__ GroupItem group_item(const GroupArgs& ga, int M, int 
 inline int64_t whole_rounds(int64_t items) { return (items + 7) / 8 * 8; }
 
 // Moves the arguments of a product on to one group: its rows of A and C (and their scales), its
-// B, bias and column scales.
-template <int ES, int CES>
+// B, bias and column scales; with MX its block scales.
+template <int ES, int CES, bool MX = false>
 __device__ __forceinline__ void enter_group(GemmParams& p, const GroupArgs& ga, int group, int row0, int rows) {
   p.A = reinterpret_cast<const uint8_t*>(p.A) + (int64_t)row0 * p.lda * ES;
   p.B = reinterpret_cast<const uint8_t*>(p.B) + (int64_t)group * ga.stride_b * ES;
@@ -164,6 +165,10 @@ __device__ __forceinline__ void enter_group(GemmParams& p, const GroupArgs& ga, 
   if (p.bias) p.bias += (int64_t)group * p.N;
   if (p.ra) p.ra += row0;
   if (p.rb) p.rb += (int64_t)group * p.N;
+  if constexpr (MX) {
+    p.sa += (int64_t)row0 * p.ldsa;
+    p.sb += (int64_t)group * ga.stride_sb;
+  }
 }
 
 // The same for the weight gradient, whose sum runs over the group's rows: p.K becomes their

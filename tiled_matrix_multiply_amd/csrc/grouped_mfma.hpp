@@ -15,7 +15,7 @@ __global__ __launch_bounds__(C::NT) void grouped_rows_kernel(GemmParams p, Group
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS_BYTES];
   const GroupItem it = group_item(ga, p.M, C::BM, p.tiles_n, workgroup(ga), threadIdx.x & 63);
   if (it.group < 0) return;
-  enter_group<C::ES, DTypeInfo<C::CT>::bytes>(p, ga, it.group, it.row0, it.rows);
+  enter_group<C::ES, DTypeInfo<C::CT>::bytes, C::MX>(p, ga, it.group, it.row0, it.rows);
   mfma_tile<C>(p, SkSeg{}, smem, tile_pos(it.local, (it.rows + C::BM - 1) / C::BM, p.tiles_n));
 }
 
@@ -56,7 +56,7 @@ __global__ __launch_bounds__(512) void grouped_rows_mixed_kernel(const GemmParam
     if (t < 0) return;
     const GroupItem it = gs.find(large_rows, tn, t);
     GemmParams p = p0;
-    enter_group<F::ES, DTypeInfo<F::CT>::bytes>(p, ga, it.group, it.row0, it.rows);
+    enter_group<F::ES, DTypeInfo<F::CT>::bytes, F::MX>(p, ga, it.group, it.row0, it.rows);
     mfma_tile<F>(p, SkSeg{}, smem, tile_pos(it.local, large_rows(it.rows), tn));
     return;
   }
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(512) void grouped_rows_mixed_kernel(const GemmParam
     if (128 * at.tm >= it.rows || 128 * at.tn >= p0.N) continue;  // a quarter past the edge
     if (base) __syncthreads();  // the last tile's output staging has been read
     GemmParams p = p0;
-    enter_group<Q::ES, DTypeInfo<Q::CT>::bytes>(p, ga, it.group, it.row0, it.rows);
+    enter_group<Q::ES, DTypeInfo<Q::CT>::bytes, Q::MX>(p, ga, it.group, it.row0, it.rows);
     mfma_tile<Q>(p, SkSeg{}, smem, at);
   }
 }
@@ -291,6 +291,31 @@ hipError_t launch_rows_layout(const GemmParams& p, const GroupArgs& ga, int tile
 template <int DT, int CT>
 hipError_t launch_rows_type(const GemmParams& p, const GroupArgs& ga, bool b_mn, int tile, int cus, hipStream_t s) {
   return b_mn ? launch_rows_layout<DT, CT, true>(p, ga, tile, cus, s) : launch_rows_layout<DT, CT, false>(p, ga, tile, cus, s);
+}
+
+// The same tiles in MXFP4 (both operands packed along K; K, lda and ldb in bytes).  Their block scales are
+// staged beside the data for two K tiles at a time, which leaves the 128 x 128 tile three stages; K is
+// not split.
+template <int CT, int TILE> struct GroupedMxCfg;
+template <int CT> struct GroupedMxCfg<CT, GT_64> {
+  using T = MfmaCfg<E2M1, 64, 2, 2, false, false, 2, E2M1, true, 0, 1, 0, 1, CT, true>;
+};
+template <int CT> struct GroupedMxCfg<CT, GT_128> {
+  using T = MfmaCfg<E2M1, 128, 2, 4, false, false, 3, E2M1, true, 0, 1, 0, 1, CT, true>;
+};
+template <int CT> struct GroupedMxCfg<CT, GT_256> {
+  using T = MfmaCfg<E2M1, 256, 2, 4, false, false, 2, E2M1, true, 0, 1, 0, 1, CT, true>;
+};
+
+template <int CT>
+hipError_t launch_mx_type(const GemmParams& p, const GroupArgs& ga, int tile, int cus, hipStream_t s) {
+  switch (tile) {
+    case GT_64: return launch_rows_cfg<typename GroupedMxCfg<CT, GT_64>::T>(p, ga, s);
+    case GT_128: return launch_rows_cfg<typename GroupedMxCfg<CT, GT_128>::T>(p, ga, s);
+    case GT_256:
+      return launch_mixed_cfg<typename GroupedMxCfg<CT, GT_256>::T, typename GroupedMxCfg<CT, GT_128>::T>(p, ga, cus, s);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 template <int DT, int CT>

@@ -1,0 +1,210 @@
+// Products by expert in MXFP4 for few rows per group (decoding), where the weights are read once and
+// nothing else matters; and for any alignment (gfx950 only).
+//
+// As the streaming kernel of the wider types: a workgroup owns 32 columns of one group and up to 16 MF
+// of its rows, its waves share out K and meet in LDS at the end, in wave order, and weights and rows go
+// straight from global memory into the registers of scaled 16 x 16 x 128 matrix instructions.  Lane l
+// of a fragment holds row (column) l % 16 and the 32 elements k = 32 (l / 16) .. + 31 of a step of 128, 16
+// bytes, with the one scale that belongs to them.  A unit is U steps; its 4 U scale bytes of a row come
+// in one load, the same for the four lanes of the row, and each lane moves its own byte of a step down.
+#include <type_traits>
+
+#include "grouped.hpp"
+
+namespace tgemm {
+
+namespace {
+
+typedef float x_f32x4 __attribute__((ext_vector_type(4)));
+typedef int x_i32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t x_u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int NF = 2, BN = 16 * NF;  // fragments and columns of a workgroup
+
+__device__ __forceinline__ x_f32x4 mma_mx(x_u32x4 x, x_u32x4 y, x_f32x4 c, int sx, int sy) {
+  const x_i32x8 a = x_i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
+  const x_i32x8 b = x_i32x8{(int)y[0], (int)y[1], (int)y[2], (int)y[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, 0, sx, 0, sy);
+}
+
+// K and the leading dimensions of A and B are in bytes (two elements each).
+template <int MF, int U>
+__global__ __launch_bounds__(512) void mx_stream_kernel(GemmParams p, GroupArgs ga, int c_type) {
+  constexpr int BM = 16 * MF, PART = NF * MF * 64 * 16;
+  extern __shared__ __attribute__((aligned(16))) uint8_t part[];
+  const int lane = threadIdx.x & 63, NW = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const GroupItem it = group_item(ga, p.M, BM, p.tiles_n, workgroup(ga), lane);
+  if (it.group < 0) return;
+  if (c_type == F32) enter_group<1, 4, true>(p, ga, it.group, it.row0, it.rows);
+  else enter_group<1, 2, true>(p, ga, it.group, it.row0, it.rows);
+  // the row tiles of a block of columns are neighbours: they share its weights in the L2
+  const int tiles_m = (p.M + BM - 1) / BM;
+  const int m0 = it.local % tiles_m * BM, n0 = it.local / tiles_m * BN;
+  const int q = lane >> 4, l16 = lane & 15;
+
+  // Lane offsets (32 bits: the host keeps a row under 2^23 bytes) from a uniform base; rows and columns
+  // past the edge repeat the last ones and are not stored.
+  const uint8_t* const Ab = reinterpret_cast<const uint8_t*>(p.A) + (int64_t)m0 * p.lda;
+  const uint8_t* const Bb = reinterpret_cast<const uint8_t*>(p.B) + (int64_t)n0 * p.ldb;
+  const uint8_t* const Sa = p.sa + (int64_t)m0 * p.ldsa;
+  const uint8_t* const Sb = p.sb + (int64_t)n0 * p.ldsb;
+  uint32_t oa[MF], ob[NF], osa[MF], osb[NF];
+#pragma unroll
+  for (int f = 0; f < MF; ++f) {
+    const uint32_t r = (uint32_t)min(16 * f + l16, p.M - 1 - m0);
+    oa[f] = r * (uint32_t)p.lda + 16 * q;
+    osa[f] = r * (uint32_t)p.ldsa;
+  }
+#pragma unroll
+  for (int f = 0; f < NF; ++f) {
+    const uint32_t r = (uint32_t)min(16 * f + l16, p.N - 1 - n0);
+    ob[f] = r * (uint32_t)p.ldb + 16 * q;
+    osb[f] = r * (uint32_t)p.ldsb;
+  }
+
+  struct Unit {
+    x_u32x4 b[NF][U], a[MF][U];
+    uint32_t sb[NF][U], sa[MF][U];
+  };
+  auto load = [&](int u, Unit& t) {
+    const int64_t k = (int64_t)u * (64 * U);
+    const uint8_t *as = Ab + k, *bs = Bb + k, *sas = Sa + (int64_t)u * (4 * U), *sbs = Sb + (int64_t)u * (4 * U);
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+#pragma unroll
+      for (int s = 0; s < U; ++s) __builtin_memcpy(&t.b[f][s], bs + ob[f] + 64 * s, 16);
+      __builtin_memcpy(t.sb[f], sbs + osb[f], 4 * U);
+    }
+#pragma unroll
+    for (int f = 0; f < MF; ++f) {
+#pragma unroll
+      for (int s = 0; s < U; ++s) __builtin_memcpy(&t.a[f][s], as + oa[f] + 64 * s, 16);
+      __builtin_memcpy(t.sa[f], sas + osa[f], 4 * U);
+    }
+  };
+  x_f32x4 acc[NF][MF];
+#pragma unroll
+  for (int j = 0; j < NF; ++j)
+#pragma unroll
+    for (int f = 0; f < MF; ++f) acc[j][f] = x_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto mul = [&](const Unit& t) {
+#pragma unroll
+    for (int s = 0; s < U; ++s)
+#pragma unroll
+      for (int j = 0; j < NF; ++j)
+#pragma unroll
+        for (int f = 0; f < MF; ++f)
+          acc[j][f] = mma_mx(t.b[j][s], t.a[f][s], acc[j][f], (int)(t.sb[j][s] >> (8 * q)), (int)(t.sa[f][s] >> (8 * q)));
+  };
+  // One step of 128 elements that may end early: a lane's 32 elements are there or not (K is a whole
+  // number of blocks); what is not there is 0 with scale 2^0.
+  auto rest_step = [&](int s) {
+    const bool there = (int64_t)s * 64 + 16 * q < p.K;
+    x_u32x4 a[MF], b[NF];
+    int sa[MF], sb[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      b[f] = x_u32x4{0u, 0u, 0u, 0u};
+      sb[f] = 127;
+      if (there) {
+        __builtin_memcpy(&b[f], Bb + (int64_t)s * 64 + ob[f], 16);
+        sb[f] = Sb[(int64_t)s * 4 + q + osb[f]];
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < MF; ++f) {
+      a[f] = x_u32x4{0u, 0u, 0u, 0u};
+      sa[f] = 127;
+      if (there) {
+        __builtin_memcpy(&a[f], Ab + (int64_t)s * 64 + oa[f], 16);
+        sa[f] = Sa[(int64_t)s * 4 + q + osa[f]];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NF; ++j)
+#pragma unroll
+      for (int f = 0; f < MF; ++f) acc[j][f] = mma_mx(b[j], a[f], acc[j][f], sb[j], sa[f]);
+  };
+
+  // Whole units over the waves in turn, two in flight each; the steps after the last whole unit go to
+  // one wave each, before its units.
+  const int steps = (int)(((int64_t)p.K + 63) / 64), units = p.K / (64 * U), first = units * U;
+  for (int s = first + wave; s < steps; s += NW) rest_step(s);
+  if (wave < units) {
+    Unit x, y;
+    int b = wave;
+    load(b, x);
+    for (; b + 2 * NW < units; b += 2 * NW) {
+      load(b + NW, y);
+      mul(x);
+      load(b + 2 * NW, x);
+      mul(y);
+    }
+    if (b + NW < units) {
+      load(b + NW, y);
+      mul(x);
+      mul(y);
+    } else {
+      mul(x);
+    }
+  }
+
+  x_f32x4* const mine = reinterpret_cast<x_f32x4*>(part + wave * PART);
+#pragma unroll
+  for (int j = 0; j < NF; ++j)
+#pragma unroll
+    for (int f = 0; f < MF; ++f) mine[(j * MF + f) * 64 + lane] = acc[j][f];
+  __syncthreads();
+
+  // A lane of fragment (j, f) holds row 16 f + l16 and, in register r, column 16 j + 4 q + r.
+  auto finish = [&](auto ct) {
+    constexpr int CT = decltype(ct)::value;
+    for (int i = threadIdx.x; i < NF * MF * 64; i += blockDim.x) {
+      const int l = i & 63, jf = i >> 6;
+      const int m = m0 + 16 * (jf % MF) + (l & 15), n = n0 + 16 * (jf / MF) + 4 * (l >> 4);
+      if (m >= p.M || n >= p.N) continue;
+      float bj[4], cin[4];  // all reads together, past the edge the last column once more
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int col = min(n + e, p.N - 1);
+        bj[e] = (p.epi & EPI_BIAS) ? p.bias[col] : 0.0f;
+        cin[e] = p.beta != 0.0f ? load_as_float<CT>(p.C, (int64_t)m * p.ldc + col) : 0.0f;
+      }
+      x_f32x4 v = x_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int w = 0; w < NW; ++w) v += reinterpret_cast<const x_f32x4*>(part + w * PART)[jf * 64 + l];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < p.N)
+          store_from_float<CT>(p.C, (int64_t)m * p.ldc + n + e, epilogue_value<CT>(v[e], p.alpha, p.beta, cin[e], bj[e], p.epi));
+    }
+  };
+  if (c_type == F32) finish(std::integral_constant<int, F32>{});
+  else if (c_type == F16) finish(std::integral_constant<int, F16>{});
+  else finish(std::integral_constant<int, BF16>{});
+}
+
+template <int MF, int U>
+hipError_t launch_cfg(GemmParams p, GroupArgs ga, int c_type, int waves, hipStream_t s) {
+  p.tiles_n = (p.N + BN - 1) / BN;
+  const int64_t grid = whole_rounds(max_row_tiles(p.M, ga.groups, 16 * MF) * p.tiles_n);
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  return launch_in_slices(grid, 64 * waves, [&](int64_t first, unsigned n) {
+    ga.first = (int)first;
+    hipLaunchKernelGGL((mx_stream_kernel<MF, U>), dim3(n), dim3(64 * waves), waves * NF * MF * 64 * 16, s, p, ga, c_type);
+  });
+}
+
+}  // namespace
+
+// rows: 16, 32 or 64 rows of C per workgroup.
+hipError_t launch_stream_mx(const GemmParams& p, const GroupArgs& ga, int c_type, int rows, int waves, hipStream_t s) {
+  switch (rows) {
+    case 16: return launch_cfg<1, 4>(p, ga, c_type, waves, s);
+    case 32: return launch_cfg<2, 2>(p, ga, c_type, waves, s);
+    case 64: return launch_cfg<4, 2>(p, ga, c_type, waves, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace tgemm
