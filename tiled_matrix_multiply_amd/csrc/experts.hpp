@@ -19,6 +19,7 @@ struct RouteArgs {
   int32_t* place;
   int64_t* offsets;
   uint8_t* ws;  // tokens of each expert in each block, route_row_bytes(E) bytes a block; null: one block
+  int run_lanes;  // log2 of the lanes that hold a run of experts; -1: runs do not fit the lanes
 };
 
 struct RouteGradArgs {
@@ -34,7 +35,7 @@ struct RouteGradArgs {
 };
 
 // Tokens of one workgroup of the router, at most 64: a token is a bit of a 64-bit mask there.
-inline int route_block_tokens(int64_t T) { return T <= 64 ? 64 : T <= 16384 ? 16 : T <= 32768 ? 32 : 64; }
+inline int route_block_tokens(int64_t T) { return T <= 64 ? 64 : T <= 4096 ? 16 : T <= 8192 ? 32 : 64; }
 inline int64_t route_blocks(int64_t T) { return (T + route_block_tokens(T) - 1) / route_block_tokens(T); }
 constexpr __host__ __device__ int64_t route_row_bytes(int64_t E) { return (E + 15) / 16 * 16; }
 

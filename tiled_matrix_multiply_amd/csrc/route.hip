@@ -3,8 +3,14 @@
 //
 // A token belongs to L lanes of a wave, each of them holding V neighbouring experts (L V >= E), so that
 // the order of lanes is the order of experts: of equal keys the lowest lane's first one is the lower
-// expert.  `top` rounds of a maximum over the lanes choose the experts; what a lane has lost in a round
-// it takes out of its own values.
+// expert.  Each lane sorts its keys once (as integers in the keys' order, with the place in the lane in
+// their last bits), and `top` rounds of a maximum over the lanes' heads choose the experts.
+//
+// Keys are computed in fp32 with a bound on their error.  Where two neighbours in the order, or the last
+// chosen and the first that was not, are nearer than the bound allows and not made of the same numbers,
+// the token is chosen again in 64 bits by the whole wave (choose, below; with random logits and biases
+// one token in some hundreds, which takes 0.3 us of the 8191 x 256 below; with all of them in 64 bits the
+// kernel took 51 us).
 //
 // The order of the rows needs no sorting: within a workgroup of up to 64 tokens each expert has a mask
 // with a bit for each token (set in any order, the same in the end), and a pair's rank there is the
@@ -67,7 +73,6 @@ __device__ __forceinline__ S sum_across(S v) {
   return across<L>(v, [](S a, S b) { return a + b; });
 }
 
-__device__ __forceinline__ float exp_of(float v) { return expf(v); }
 __device__ __forceinline__ double exp_of(double v) { return exp(v); }
 
 // The L lanes' part of a wave's ballot.
@@ -87,8 +92,75 @@ struct Best2 {
   }
 };
 
-// The choice of one token's experts: lane j of the token's L gets the j-th (-1: none) and its logit.
-// x: the lane's logits, -infinity where there is no expert; keys are computed in type S.
+// Integers in the order of the values; 0 is below all of them.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true));
+}
+template <int L>
+__device__ __forceinline__ uint32_t max_across(uint32_t v) {
+  v = max_dpp<0x128>(v);
+  v = max_dpp<0x124>(v);
+  v = max_dpp<0x122>(v);
+  v = max_dpp<0x121>(v);
+  if constexpr (L == 64)
+    v = max(max((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16)),
+            max((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48)));
+  return v;
+}
+
+// Falling order, by Batcher's odd-even merging of runs (63 exchanges for 16 values, two instructions each).
+template <int V>
+__device__ __forceinline__ void sort_falling(uint32_t (&v)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < V; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < V && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t a = v[i + j], b = v[i + j + k];
+            v[i + j] = max(a, b);
+            v[i + j + k] = min(a, b);
+          }
+}
+
+// The lowest lane of a token's L (as an index among them) where `mine` holds; some lane's has to.
+template <int L>
+__device__ __forceinline__ int first_lane(bool mine, int lane) {
+  const uint64_t m = __ballot(mine);
+  if constexpr (L == 64) return (int)__builtin_ctzll(m);
+  const uint32_t half = lane & 32 ? (uint32_t)(m >> 32) : (uint32_t)m;
+  return (int)__builtin_ctz(half >> (lane & 16));
+}
+
+__device__ __forceinline__ float quick_exp(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504f); }
+
+// The sum of a lane's values, pairwise.
+template <int V>
+__device__ __forceinline__ float lane_sum(const float (&v)[V]) {
+  float s[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) s[i] = v[i];
+#pragma unroll
+  for (int d = 1; d < V; d *= 2)
+#pragma unroll
+    for (int i = 0; i + d < V; i += 2 * d) s[i] += s[i + d];
+  return s[0];
+}
+
+// The choice of one token's experts with keys in type S: lane j of the token's L gets the j-th (-1: none)
+// and its logit.  x: the lane's logits, -infinity where there is no expert.
 template <int L, int V, class S>
 __device__ __forceinline__ void choose(const RouteArgs& p, const float (&x)[V], int lane, int sub, S rcp_sum, float x_max,
                                        int& chosen, float& chosen_x) {
@@ -190,17 +262,238 @@ __device__ __forceinline__ void choose(const RouteArgs& p, const float (&x)[V], 
   }
 }
 
+// ---- the same in fp32, where that is certain ----
+
+// How a token's experts lie in its L lanes: each run of experts begins with a lane of its own and has a
+// power of two of lanes, V experts to a lane, so that runs of any size meet in a few steps.  Without runs
+// (or where they do not fit so) one after another.
+struct Layout {
+  int runs, size, lanes_log2;  // experts and lanes of a run
+  __device__ __forceinline__ Layout(const RouteArgs& p) {
+    const bool apart = p.groups > 1 && p.run_lanes >= 0;
+    runs = apart ? p.groups : 1;
+    size = p.E / runs;
+    lanes_log2 = apart ? p.run_lanes : 6;
+  }
+  template <int V>
+  __device__ __forceinline__ int in_run(int sub) const {
+    return (sub & ((1 << lanes_log2) - 1)) * V;
+  }
+  template <int V>
+  __device__ __forceinline__ int expert(int sub) const {  // the lane's first
+    return (sub >> lanes_log2) * size + in_run<V>(sub);
+  }
+  template <int V>
+  __device__ __forceinline__ int count(int sub) const {  // and how many it has
+    return (sub >> lanes_log2) < runs ? min(max(size - in_run<V>(sub), 0), V) : 0;
+  }
+};
+
+// The n <= V logits of a lane from expert e on, -infinity after them.
+template <int V>
+__device__ __forceinline__ void load_logits(const RouteArgs& p, int64_t t, int e, int n, float (&x)[V]) {
+  const int64_t at = t * p.ldx + e;
+  if (n == V && V > 1) {  // all loads together, of any alignment
+    if (p.x_type == F32) {
+      __builtin_memcpy(x, reinterpret_cast<const float*>(p.x) + at, 4 * V);
+    } else {
+      uint32_t w[(V + 1) / 2] = {};
+      __builtin_memcpy(w, reinterpret_cast<const uint16_t*>(p.x) + at, 2 * V);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const uint32_t h = (w[i / 2] >> (16 * (i & 1))) & 0xffffu;
+        x[i] = p.x_type == F16 ? f16_bits_to_float(h) : bf16_bits_to_float(h);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = i < n ? load_logit(p.x, at + i, p.x_type) : kNone;
+  }
+}
+
+// Whether the lane's run of experts is kept.  w: the two best of the lane; a run's worth is off by at
+// most half of `slack`; sure turns false where that could decide.  A run's rank is the number of lanes of
+// runs that are worth more: the 16 lanes of a token are turned around, of 64 one lane of each run is read.
+template <int L>
+__device__ __forceinline__ bool keep_run(const RouteArgs& p, Best2<float> w, int sub, float slack, bool& sure) {
+  auto meet = [&](float a, float b) {
+    w.add(a);
+    w.add(b);
+  };
+  const int lm = p.run_lanes, m = 1 << lm;
+  if (lm > 0) meet(dpp<0xb1>(w.a), dpp<0xb1>(w.b));    // lanes 1 0 3 2
+  if (lm > 1) meet(dpp<0x4e>(w.a), dpp<0x4e>(w.b));    // lanes 2 3 0 1
+  if (lm > 2) meet(dpp<0x141>(w.a), dpp<0x141>(w.b));  // eight lanes mirrored: the other four
+  if (lm > 3) meet(dpp<0x140>(w.a), dpp<0x140>(w.b));  // sixteen mirrored: the other eight
+  if constexpr (L == 64) {
+    if (lm > 4) meet(__shfl_xor(w.a, 16), __shfl_xor(w.b, 16));
+    if (lm > 5) meet(__shfl_xor(w.a, 32), __shfl_xor(w.b, 32));
+  }
+  const float t = p.group_top == 2 && w.b != kNone ? w.a + w.b : w.a;
+  const int first = sub & ~(m - 1);
+  int over = 0, near = 0;  // lanes (of 64: runs) worth more for certain, and those that may be
+  auto rank = [&](float u, int from) {
+    const bool own = ((from ^ sub) & ~(m - 1)) == 0;
+    const bool more = slack == 0.0f && (u > t || (u == t && from < first));
+    over += !own && (slack == 0.0f ? more : u - t > slack);
+    near += !own && (slack == 0.0f ? more : !(t - u > slack));
+  };
+  int most = p.top_groups;
+  if constexpr (L == 64) {
+    for (int g = 0; g < p.groups; ++g) rank(lane_value(t, g << lm), g << lm);
+  } else {
+#define TGEMM_TURN(r) rank(dpp<0x120 + r>(t), (sub - r) & 15)
+    TGEMM_TURN(1); TGEMM_TURN(2); TGEMM_TURN(3); TGEMM_TURN(4); TGEMM_TURN(5);
+    TGEMM_TURN(6); TGEMM_TURN(7); TGEMM_TURN(8); TGEMM_TURN(9); TGEMM_TURN(10);
+    TGEMM_TURN(11); TGEMM_TURN(12); TGEMM_TURN(13); TGEMM_TURN(14); TGEMM_TURN(15);
+#undef TGEMM_TURN
+    most <<= lm;
+  }
+  if (t == kNone) return false;  // no expert there
+  if (over < most && near >= most) sure = false;
+  return near < most;
+}
+
+// choose() in fp32; false in the lanes of a token for which it is not certain.
+template <int L, int V>
+__device__ __forceinline__ bool choose_quick(const RouteArgs& p, const Layout& lay, const float (&x)[V], int64_t t,
+                                             int lane, int sub, float x_max, float rcp_sum, int& chosen,
+                                             float& chosen_x) {
+  constexpr uint32_t LOW = V - 1;
+  const int e0 = lay.expert<V>(sub), n = lay.count<V>(sub);
+  const bool scored = p.bias || (p.groups > 1 && p.group_top == 2);
+  float key[V], s[V];
+  float slack = 0.0f;  // bound on the error of a score
+  if (scored) {
+    // Relative errors: the exponential's argument is off by half a step or two of itself, the function
+    // and the reciprocal by a step.  z exp(-z) <= 0.37, and z s(-z) falls from z = 1.3 on, so that the
+    // argument's part is largest at the largest score.  softmax: its sum is off by up to 10 half steps.
+    float top;
+    if (p.score) {
+      top = __builtin_amdgcn_rcpf(1.0f + quick_exp(-x_max));
+      slack = top * (0x1p-21f + fmaxf(1.3f, -x_max) * 0x1p-22f);
+    } else {
+      top = rcp_sum;
+      slack = top * 0x1p-19f;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      s[i] = p.score ? __builtin_amdgcn_rcpf(1.0f + quick_exp(-x[i])) : quick_exp(x[i] - x_max) * rcp_sum;
+  }
+  if (p.bias) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float b = i < n ? p.bias[e0 + i] : kNone;
+      const float k = s[i] + b;
+      key[i] = x[i] == kNone || b == kNone ? kNone : k != k ? -kNone : k;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = x[i] != x[i] ? -kNone : x[i];
+  }
+  bool sure = true;
+  if (p.groups > 1) {
+    Best2<float> w{kNone, kNone};
+    const bool by_score = !p.bias && p.group_top == 2;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float v = by_score && key[i] != kNone ? s[i] : key[i];
+      w.add(v != v ? -kNone : v);
+    }
+    // (a run's sum of two: twice the error, and the rounding of the sum, which is that of the keys too)
+    const float worst = max_across<L>(fmaxf(fabsf(w.a == kNone ? 0.0f : w.a), fabsf(w.b == kNone ? 0.0f : w.b)));
+    const bool exact = !scored;
+    const bool kept = keep_run<L>(p, w, sub, exact ? 0.0f : 4.0f * slack + 0x1p-21f * worst, sure);
+    if (!kept) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = kNone;
+    }
+  }
+  uint32_t u[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    u[i] = key[i] == kNone ? 0u : (ordered(key[i] + 0.0f) & ~LOW) | (LOW - i);  // (+ 0: one zero)
+  sort_falling<V>(u);
+  chosen = -1;
+  uint32_t mine = 0;
+  // The best head of the token's lanes, the lowest lane's of equal ones (their last bits are places, not
+  // values), and its expert; it leaves its lane.
+  auto next = [&](int& e) {
+    const uint32_t head = u[0] & ~LOW, best = max_across<L>(head);
+    const int first = first_lane<L>(head == best, lane);
+    const int i = (int)(LOW - (u[0] & LOW));
+    if constexpr (L == 64) e = lay.expert<V>(first) + __builtin_amdgcn_readlane(i, first);
+    else e = lay.expert<V>(first) + (V > 1 ? __shfl(i, (lane & 48) + first) : 0);
+    if (sub == first) {
+#pragma unroll
+      for (int q = 0; q + 1 < V; ++q) u[q] = u[q + 1];
+      u[V - 1] = 0u;
+    }
+    return best;
+  };
+  uint32_t last = 0;
+  int e_last = 0;
+  for (int j = 0; j < p.top; ++j) {
+    last = next(e_last);
+    if (sub == j) {
+      chosen = last ? e_last : -1;
+      mine = last;
+    }
+  }
+  // Is the order certain?  Neighbours of the chosen, in their lanes.
+  const float* const bias = p.bias;
+  auto apart = [&](uint32_t a, uint32_t b) {  // a >= b, without their last bits
+    if (!bias) return a != b;  // the logits themselves
+    // what the last bits were worth, and two roundings
+    const float fa = from_ordered(a), fb = from_ordered(b);
+    return fa - fb > 2.0f * slack + (V + 4) * 0x1p-23f * fmaxf(fabsf(fa), fabsf(fb));
+  };
+  chosen_x = chosen >= 0 ? load_logit(p.x, t * p.ldx + chosen, p.x_type) : 0.0f;
+  const float b_mine = chosen >= 0 && bias ? bias[chosen] : 0.0f;
+  {
+    const int up = lane + 1;
+    const uint32_t u2 = (uint32_t)__shfl((int)mine, up);
+    const float x2 = __shfl(chosen_x, up), b2 = __shfl(b_mine, up);
+    if (sub + 1 < p.top && u2 && !apart(mine, u2) && !(x2 == chosen_x && b2 == b_mine)) sure = false;
+  }
+  // The last one and those that were not chosen: equal ones may follow (a few are looked at).
+  if (last) {
+    const float xl = load_logit(p.x, t * p.ldx + e_last, p.x_type), bl = bias ? bias[e_last] : 0.0f;
+    for (int more = 0;; ++more) {
+      int e;
+      const uint32_t r = next(e);
+      if (!r || apart(last, r)) break;
+      const bool same = load_logit(p.x, t * p.ldx + e, p.x_type) == xl && (bias ? bias[e] : 0.0f) == bl;
+      if (!same || more == 3) {
+        sure = false;
+        break;
+      }
+    }
+  }
+  return sure;
+}
+
 // The scores' common parts over a token: the largest logit and, for softmax, the sum of exp(x - largest).
-template <int L, int V, class S>
-__device__ __forceinline__ S softmax_sum(const float (&x)[V], float& x_max) {
+template <int L, int V>
+__device__ __forceinline__ float largest(const float (&x)[V]) {
   float m = x[0];
 #pragma unroll
   for (int i = 1; i < V; ++i) m = fmaxf(m, x[i]);
-  x_max = max_across<L>(m);
-  S sum = 0;
+  return max_across<L>(m);
+}
+template <int L, int V, class S>
+__device__ __forceinline__ S softmax_sum(const float (&x)[V], float x_max) {
+  if constexpr (sizeof(S) == 8) {
+    S sum = 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) sum += x[i] == kNone ? (S)0 : exp_of((S)x[i] - (S)x_max);
-  return sum_across<L>(sum);
+    for (int i = 0; i < V; ++i) sum += x[i] == kNone ? (S)0 : exp_of((S)x[i] - (S)x_max);
+    return sum_across<L>(sum);
+  } else {
+    float e[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) e[i] = x[i] == kNone ? 0.0f : expf(x[i] - x_max);
+    return sum_across<L>(lane_sum<V>(e));
+  }
 }
 
 // Weight of the lane's chosen expert among the token's: p.top lanes hold one each.
@@ -221,36 +514,70 @@ __device__ __forceinline__ float weight_of(const RouteArgs& p, int chosen, float
   return there ? p.scale * (s / all) : 0.0f;
 }
 
-// THREADS: of a workgroup.  TB tokens of a workgroup, 64 / L of them to a wave at a time.
+// One token again in 64 bits, by the whole wave: lane j < top gets the j-th expert and its logit.
+template <int VV>
+__device__ __forceinline__ void choose_again(const RouteArgs& p, int64_t t, int lane, int& chosen, float& cx) {
+  float x[VV];
+#pragma unroll
+  for (int i = 0; i < VV; ++i) {
+    const int e = lane * VV + i;
+    x[i] = e < p.E ? load_logit(p.x, t * p.ldx + e, p.x_type) : kNone;
+  }
+  float x_max = 0.0f;
+  double sum = 1.0;
+  if (!p.score && (p.bias || (p.groups > 1 && p.group_top == 2))) {
+    x_max = largest<64, VV>(x);
+    sum = softmax_sum<64, VV, double>(x, x_max);
+  }
+  choose<64, VV, double>(p, x, lane, lane, 1.0 / sum, x_max, chosen, cx);
+}
+
+// TB tokens of a workgroup, 64 / L of them to a wave at a time.
 template <int L, int V, int THREADS>
 __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs p, int TB) {
   __shared__ unsigned long long mask[1024];
   __shared__ int start[1024 + 1];
   __shared__ int16_t pick[64 * 32];
   __shared__ int part[THREADS / 64];
-  const int tid = threadIdx.x, lane = tid & 63, sub = lane & (L - 1), wave = tid >> 6;
+  constexpr int VV = (L * V + 63) / 64;
+  const int tid = threadIdx.x, lane = tid & 63, sub = lane & (L - 1), wave = tid >> 6, threads = blockDim.x;
   const int64_t t0 = (int64_t)blockIdx.x * TB;
   const int here = (int)min((int64_t)TB, p.T - t0);
-  for (int e = tid; e < p.E; e += THREADS) mask[e] = 0ull;
+  for (int e = tid; e < p.E; e += threads) mask[e] = 0ull;
   __syncthreads();
-  constexpr int TW = 64 / L, STEP = THREADS / 64 * TW;
-  for (int base = wave * TW; base < here; base += STEP) {  // (the same for all lanes of a wave)
+  constexpr int TW = 64 / L;
+  const Layout lay(p);
+  for (int base = wave * TW; base < here; base += threads / 64 * TW) {  // (the same for all lanes of a wave)
     const int local = base + lane / L;
     const bool live = local < here;
     const int64_t t = t0 + (live ? local : here - 1);
     float x[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = sub * V + i;
-      x[i] = e < p.E ? load_logit(p.x, t * p.ldx + e, p.x_type) : kNone;
+    load_logits<V>(p, t, lay.expert<V>(sub), lay.count<V>(sub), x);
+    const bool scored = p.bias || (p.groups > 1 && p.group_top == 2);
+    float x_max = 0.0f, sum = 1.0f;
+    if (scored || (!p.score && !p.renorm)) {
+      x_max = largest<L, V>(x);
+      if (!p.score) sum = softmax_sum<L, V, float>(x, x_max);
     }
-    float x_max = 0.0f;
-    double sum = 1.0;
-    if (!p.score && (!p.renorm || p.bias || (p.groups > 1 && p.group_top == 2))) sum = softmax_sum<L, V, double>(x, x_max);
-    int chosen;
-    float cx;
-    choose<L, V, double>(p, x, lane, sub, 1.0 / sum, x_max, chosen, cx);
-    const float w = weight_of<L, V>(p, chosen, cx, x_max, (float)sum);
+    int chosen = -1;
+    float cx = 0.0f;
+    bool sure = false;
+    if (p.run_lanes >= 0) sure = choose_quick<L, V>(p, lay, x, t, lane, sub, x_max, 1.0f / sum, chosen, cx);
+    for (uint64_t again = __ballot(!sure); again;) {
+      const int from = (int)__builtin_ctzll(again) & ~(L - 1);  // the token's first lane
+      again &= ~((L == 64 ? ~0ull : 0xffffull) << from);
+      const int at = base + from / L;
+      int c;
+      float v;
+      choose_again<VV>(p, t0 + (at < here ? at : here - 1), lane, c, v);
+      const int cs = __shfl(c, sub);
+      const float vs = __shfl(v, sub);
+      if ((lane & ~(L - 1)) == from) {
+        chosen = cs;
+        cx = vs;
+      }
+    }
+    const float w = weight_of<L, V>(p, chosen, cx, x_max, sum);
     if (live && sub < p.top) {
       pick[local * p.top + sub] = (int16_t)chosen;
       const int64_t at = t * p.top + sub;
@@ -262,7 +589,7 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs p, int TB) {
   __syncthreads();
   if (!p.ws) {  // the only block: where each expert's rows start
     int carry = 0;
-    for (int base = 0; base < p.E; base += THREADS) {
+    for (int base = 0; base < p.E; base += threads) {
       const int e = base + tid;
       int v = e < p.E ? __popcll(mask[e]) : 0;
       const int own = v;
@@ -274,7 +601,7 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs p, int TB) {
       if (lane == 63) part[wave] = v;
       __syncthreads();
       int before = carry, all = 0;
-      for (int w = 0; w < THREADS / 64; ++w) {
+      for (int w = 0; w < threads / 64; ++w) {
         if (w < wave) before += part[w];
         all += part[w];
       }
@@ -288,9 +615,9 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs p, int TB) {
     if (tid == 0) p.offsets[p.E] = carry;
   } else {
     uint8_t* const row = p.ws + blockIdx.x * route_row_bytes(p.E);
-    for (int e = tid; e < route_row_bytes(p.E); e += THREADS) row[e] = e < p.E ? (uint8_t)__popcll(mask[e]) : 0;
+    for (int e = tid; e < route_row_bytes(p.E); e += threads) row[e] = e < p.E ? (uint8_t)__popcll(mask[e]) : 0;
   }
-  for (int i = tid; i < here * p.top; i += THREADS) {
+  for (int i = tid; i < here * p.top; i += threads) {
     const int e = pick[i], local = i / p.top;
     int at = -1;
     if (e >= 0) at = __popcll(mask[e] & ((1ull << local) - 1)) + (p.ws ? 0 : start[e]);
@@ -311,22 +638,45 @@ __global__ __launch_bounds__(256) void route_place_kernel(RouteArgs p, int TB, i
   const int per = (int)(row / 16);  // 16 experts to a thread
   const int rows = 256 / per, c = tid % per, r = tid / per;
   if (r < rows) {
-    int all[16] = {}, mine[16] = {};
-    for (int b = r; b < blocks; b += rows) {
-      r_u32x4 v;
-      __builtin_memcpy(&v, p.ws + b * row + 16 * c, 16);
+    // 16 counts of a row in four words, taken apart into sums of 16 bits each (flushed before they could
+    // pass 65535: 1000 rows of at most 64); eight loads in flight
+    auto flush = [&](uint32_t (&w)[8], int* to) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int n = (v[i / 4] >> (8 * (i % 4))) & 255;
-        all[i] += n;
-        mine[i] += b < b0 ? n : 0;
+      for (int i = 0; i < 8; ++i) {
+        const int e = 16 * c + 4 * (i / 2) + (i & 1);  // even words: bytes 0 and 2, odd: 1 and 3
+        atomicAdd(&to[e], (int)(w[i] & 0xffffu));
+        atomicAdd(&to[e + 2], (int)(w[i] >> 16));
+        w[i] = 0;
+      }
+    };
+    uint32_t all[8] = {}, mine[8] = {};
+    int held = 0;
+    for (int b = r; b < blocks; b += 8 * rows) {
+      r_u32x4 v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        __builtin_memcpy(&v[q], p.ws + min(b + q * rows, blocks - 1) * row + 16 * c, 16);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int at = b + q * rows;
+        const uint32_t in = at < blocks ? 0x00ff00ffu : 0u, below = at < b0 ? 0x00ff00ffu : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          all[2 * i] += v[q][i] & in;
+          all[2 * i + 1] += (v[q][i] >> 8) & in;
+          mine[2 * i] += v[q][i] & below;
+          mine[2 * i + 1] += (v[q][i] >> 8) & below;
+        }
+      }
+      held += 8;
+      if (held >= 1000) {
+        flush(all, total);
+        flush(mine, before);
+        held = 0;
       }
     }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      atomicAdd(&total[16 * c + i], all[i]);
-      atomicAdd(&before[16 * c + i], mine[i]);
-    }
+    flush(all, total);
+    flush(mine, before);
   }
   __syncthreads();
   int carry = 0;
@@ -405,6 +755,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
       const int k = sub * V + i;
       x[i] = k < p.E ? load_logit(p.x, tt * p.ldx + k, p.x_type) : kNone;
     }
+    x_max = largest<L, V>(x);
     sum = softmax_sum<L, V, float>(x, x_max);
     uint32_t taken = 0;  // which of the lane's experts were chosen
     for (int j = 0; j < p.top; ++j) {
@@ -457,25 +808,48 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
   }
 }
 
-template <int L, int V, int THREADS>
+template <int L, int V, int MOST>
 hipError_t route_launch(const RouteArgs& p, int TB, hipStream_t s) {
   const int64_t blocks = p.T ? ((int64_t)p.T + TB - 1) / TB : 1;  // without tokens the offsets are written
-  hipLaunchKernelGGL((route_kernel<L, V, THREADS>), dim3((unsigned)blocks), dim3(THREADS), 0, s, p, TB);
+  // a workgroup's tokens all at once, if its waves can be that many
+  const int tokens = p.T < TB ? p.T : TB;
+  int threads = (tokens * L + 255) / 256 * 256;
+  threads = threads < 256 ? 256 : threads > MOST ? MOST : threads;
+  if (blocks * threads > 0xffffffffLL) threads = 256;  // the runtime counts work items in 32 bits
+  hipLaunchKernelGGL((route_kernel<L, V, MOST>), dim3((unsigned)blocks), dim3(threads), 0, s, p, TB);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// (Work items of a launch are counted in 32 bits: at most 2^29 tokens, 64 to a workgroup of 256 threads.)
-hipError_t launch_route(const RouteArgs& p, hipStream_t s) {
+hipError_t launch_route(const RouteArgs& args, hipStream_t s) {
+  RouteArgs p = args;
   const int TB = route_block_tokens(p.T);
+  // Lanes of a token: 16 hold a choice of at most 16; a few tokens are over sooner with 64 lanes each, and
+  // so many experts do not fit 16.  Experts of a lane: the fewest that hold all of them, runs of them in
+  // lanes of their own.
+  auto fits = [&](int L, int V) {
+    if (p.groups == 1) {
+      p.run_lanes = 6;
+      return p.E <= L * V;
+    }
+    const int size = p.E / p.groups;
+    p.run_lanes = 0;
+    while ((V << p.run_lanes) < size) ++p.run_lanes;
+    return p.groups << p.run_lanes <= L;
+  };
   hipError_t e;
+  if (p.top > 16 || p.T <= 16 || !fits(16, 16))
+    e = fits(64, 1)    ? route_launch<64, 1, 1024>(p, TB, s)
+        : fits(64, 4)  ? route_launch<64, 4, 1024>(p, TB, s)
+        : fits(64, 16) ? route_launch<64, 16, 512>(p, TB, s)
+                       : (p.run_lanes = -1, route_launch<64, 16, 512>(p, TB, s));  // all in 64 bits
+  else
+    e = fits(16, 1)   ? route_launch<16, 1, 1024>(p, TB, s)
+        : fits(16, 4) ? route_launch<16, 4, 1024>(p, TB, s)
+        : fits(16, 8) ? route_launch<16, 8, 1024>(p, TB, s)
+                      : (fits(16, 16), route_launch<16, 16, 1024>(p, TB, s));
   const bool one = p.T <= 64;
-  // 16 lanes to a token hold a choice of at most 16
-  if (p.E <= 16) e = one ? route_launch<16, 1, 1024>(p, TB, s) : route_launch<16, 1, 256>(p, TB, s);
-  else if (p.E <= 64 && p.top <= 16) e = one ? route_launch<16, 4, 1024>(p, TB, s) : route_launch<16, 4, 256>(p, TB, s);
-  else if (p.E <= 256) e = one ? route_launch<64, 4, 1024>(p, TB, s) : route_launch<64, 4, 256>(p, TB, s);
-  else e = one ? route_launch<64, 16, 1024>(p, TB, s) : route_launch<64, 16, 256>(p, TB, s);
   if (e != hipSuccess || one) return e;
   const int64_t blocks = route_blocks(p.T);
   hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)(blocks < 256 ? blocks : 256)), dim3(256), 0, s, p, TB, (int)blocks);

@@ -31,7 +31,7 @@ namespace {
 using namespace tgemm::checks;
 
 constexpr int64_t kMaxGroups = 65535;
-constexpr int64_t kMaxTokens = int64_t(1) << 29;  // of the router, whose launch has 4 threads a token
+constexpr int64_t kMaxTokens = int64_t(1) << 29;  // of the router: 4 threads a token at least, counted in 32 bits
 constexpr int64_t kMaxExperts = 1024, kMaxTop = 32, kMaxRuns = 64;
 
 // Whether a result overlaps an operand or another result.
@@ -304,7 +304,7 @@ gemm_status_t gemm_route(gemm_handle_t h, void* stream, int64_t tokens, int64_t 
   if (st != GEMM_OK) return st;
   const tgemm::RouteArgs p{logits, ldl, (int)tokens, (int)experts, (int)top, (int)x_type, (int)score, bias, (int)groups,
                            (int)top_groups, group_top, renorm, scale, expert, weight, place, offsets,
-                           tokens <= 64 ? nullptr : static_cast<uint8_t*>(workspace)};
+                           tokens <= 64 ? nullptr : static_cast<uint8_t*>(workspace), 0};
   tgemm::DeviceGuard g(h->device);
   return status(tgemm::launch_route(p, static_cast<hipStream_t>(stream)));
 }
