@@ -19,7 +19,10 @@ struct RouteArgs {
   int32_t* place;
   int64_t* offsets;
   uint8_t* ws;  // tokens of each expert in each block, route_row_bytes(E) bytes a block; null: one block
+  // set by the launcher
   int run_lanes;  // log2 of the lanes that hold a run of experts; -1: runs do not fit the lanes
+  int run_size;   // experts of a run
+  int per_top;    // i / top is i * per_top >> 16 for i up to 2048 (off by less than i / 65536 < 1 / top)
 };
 
 struct RouteGradArgs {

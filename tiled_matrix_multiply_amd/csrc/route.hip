@@ -8,9 +8,8 @@
 //
 // Keys are computed in fp32 with a bound on their error.  Where two neighbours in the order, or the last
 // chosen and the first that was not, are nearer than the bound allows and not made of the same numbers,
-// the token is chosen again in 64 bits by the whole wave (choose, below; with random logits and biases
-// one token in some hundreds, which takes 0.3 us of the 8191 x 256 below; with all of them in 64 bits the
-// kernel took 51 us).
+// those few are ranked by keys in 64 bits; what that cannot settle (runs of experts that are worth the
+// same, many near ones) is chosen again in 64 bits by the whole wave.
 //
 // The order of the rows needs no sorting: within a workgroup of up to 64 tokens each expert has a mask
 // with a bit for each token (set in any order, the same in the end), and a pair's rank there is the
@@ -18,6 +17,7 @@
 // table of blocks x experts counts (a byte each, at most 64), from which a second kernel takes where
 // each block's rows start.
 #include "experts.hpp"
+#include "grouped.hpp"
 
 namespace tgemm {
 
@@ -75,20 +75,19 @@ __device__ __forceinline__ S sum_across(S v) {
 
 __device__ __forceinline__ double exp_of(double v) { return exp(v); }
 
-// The L lanes' part of a wave's ballot.
-template <int L>
-__device__ __forceinline__ uint64_t own_bits(uint64_t ballot, int lane) {
-  return L == 64 ? ballot : (ballot >> (lane & 48)) & 0xffffull;
-}
-
-// The two largest of a set, -infinity where it has fewer.
+// The two largest of a set without NaN, -infinity where it has fewer.
 template <class S>
 struct Best2 {
   S a, b;
   __device__ __forceinline__ void add(S v) {
-    const S low = v < a ? v : a;
-    a = v < a ? a : v;
-    b = b < low ? low : b;
+    if constexpr (sizeof(S) == 4) {
+      b = __builtin_amdgcn_fmed3f(a, b, v);
+      a = v > a ? v : a;
+    } else {
+      const S low = v < a ? v : a;
+      a = v < a ? a : v;
+      b = b < low ? low : b;
+    }
   }
 };
 
@@ -159,121 +158,16 @@ __device__ __forceinline__ float lane_sum(const float (&v)[V]) {
   return s[0];
 }
 
-// The choice of one token's experts with keys in type S: lane j of the token's L gets the j-th (-1: none)
-// and its logit.  x: the lane's logits, -infinity where there is no expert.
-template <int L, int V, class S>
-__device__ __forceinline__ void choose(const RouteArgs& p, const float (&x)[V], int lane, int sub, S rcp_sum, float x_max,
-                                       int& chosen, float& chosen_x) {
-  constexpr S none = -(S)__builtin_inf();
-  const int e0 = sub * V;
-  auto score = [&](float v) {
-    return p.score ? (S)1 / ((S)1 + exp_of(-(S)v)) : exp_of((S)v - (S)x_max) * rcp_sum;
-  };
-  S key[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    S k = x[i];
-    if (p.bias) {
-      const float b = e0 + i < p.E ? p.bias[e0 + i] : kNone;
-      k = x[i] == kNone || b == kNone ? none : score(x[i]) + (S)b;
-    }
-    key[i] = k != k ? -none : k;
-  }
-  if (p.groups > 1) {
-    // What each run of experts is worth: in the lane h < groups of the token, and in turn of h + L, ...
-    const int size = p.E / p.groups;
-    const bool by_score = !p.bias && p.group_top == 2;
-    S worth[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      worth[i] = by_score && key[i] != none ? score(x[i]) : key[i];
-      if (worth[i] != worth[i]) worth[i] = -none;
-    }
-    constexpr int GL = 64 / L;  // up to 64 runs
-    S total[GL];
-#pragma unroll
-    for (int q = 0; q < GL; ++q) total[q] = none;
-    for (int g = 0; g < p.groups; ++g) {
-      Best2<S> m{none, none};
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = e0 + i;
-        m.add(e >= g * size && e < (g + 1) * size ? worth[i] : none);
-      }
-      const S a = max_across<L>(m.a);
-      // the lowest lane that holds it gives up its first
-      const uint64_t own = own_bits<L>(__ballot(m.a == a), lane);
-      const S second = max_across<L>(sub == (int)__builtin_ctzll(own | 1ull << 63) ? m.b : m.a);
-      const S t = p.group_top == 2 && second != none ? a + second : a;
-#pragma unroll
-      for (int q = 0; q < GL; ++q)
-        if (g == sub + q * L) total[q] = t;
-    }
-    uint64_t kept = 0;
-    for (int r = 0; r < p.top_groups; ++r) {
-      S m = total[0];
-#pragma unroll
-      for (int q = 1; q < GL; ++q) m = total[q] > m ? total[q] : m;
-      m = max_across<L>(m);
-      int g = 64;  // the lowest of the runs that are worth it
-#pragma unroll
-      for (int q = GL - 1; q >= 0; --q) {
-        const uint64_t own = own_bits<L>(__ballot(total[q] == m), lane);
-        if (own) g = q * L + __builtin_ctzll(own);
-      }
-      if (m == none) break;  // (all lanes of a token together)
-      kept |= 1ull << g;
-#pragma unroll
-      for (int q = 0; q < GL; ++q)
-        if (g == sub + q * L) total[q] = none;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (!((kept >> min((e0 + i) / size, 63)) & 1)) key[i] = none;
-  }
-  chosen = -1;
-  chosen_x = 0.0f;
-  for (int j = 0; j < p.top; ++j) {
-    S m = key[0];
-    int at = 0;
-    float xm = x[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i)
-      if (key[i] > m) {
-        m = key[i];
-        at = i;
-        xm = x[i];
-      }
-    const S best = max_across<L>(m);
-    const uint64_t own = own_bits<L>(__ballot(m == best), lane);
-    const int first = __builtin_ctzll(own | 1ull << 63);
-    const int from = (lane & ~(L - 1)) + first;
-    const int e = __shfl(e0 + at, from);
-    const float v = __shfl(xm, from);
-    if (sub == j) {
-      chosen = best == none ? -1 : e;
-      chosen_x = v;
-    }
-    if (sub == first) {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i == at) key[i] = none;
-    }
-  }
-}
-
-// ---- the same in fp32, where that is certain ----
-
 // How a token's experts lie in its L lanes: each run of experts begins with a lane of its own and has a
 // power of two of lanes, V experts to a lane, so that runs of any size meet in a few steps.  Without runs
 // (or where they do not fit so) one after another.
 struct Layout {
   int runs, size, lanes_log2;  // experts and lanes of a run
-  __device__ __forceinline__ Layout(const RouteArgs& p) {
-    const bool apart = p.groups > 1 && p.run_lanes >= 0;
+  __device__ __forceinline__ Layout(const RouteArgs& p, int run_lanes) {
+    const bool apart = p.groups > 1 && run_lanes >= 0;
     runs = apart ? p.groups : 1;
-    size = p.E / runs;
-    lanes_log2 = apart ? p.run_lanes : 6;
+    size = apart ? p.run_size : p.E;
+    lanes_log2 = apart ? run_lanes : 6;
   }
   template <int V>
   __device__ __forceinline__ int in_run(int sub) const {
@@ -282,6 +176,10 @@ struct Layout {
   template <int V>
   __device__ __forceinline__ int expert(int sub) const {  // the lane's first
     return (sub >> lanes_log2) * size + in_run<V>(sub);
+  }
+  template <int V>
+  __device__ __forceinline__ int of_place(int q) const {  // the expert in place q % V of lane q / V
+    return expert<V>(q / V) + q % V;
   }
   template <int V>
   __device__ __forceinline__ int count(int sub) const {  // and how many it has
@@ -299,10 +197,12 @@ __device__ __forceinline__ void load_logits(const RouteArgs& p, int64_t t, int e
     } else {
       uint32_t w[(V + 1) / 2] = {};
       __builtin_memcpy(w, reinterpret_cast<const uint16_t*>(p.x) + at, 2 * V);
+      if (p.x_type == F16) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const uint32_t h = (w[i / 2] >> (16 * (i & 1))) & 0xffffu;
-        x[i] = p.x_type == F16 ? f16_bits_to_float(h) : bf16_bits_to_float(h);
+        for (int i = 0; i < V; ++i) x[i] = f16_bits_to_float((w[i / 2] >> (16 * (i & 1))) & 0xffffu);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = bf16_bits_to_float((w[i / 2] >> (16 * (i & 1))) & 0xffffu);
       }
     }
   } else {
@@ -314,13 +214,14 @@ __device__ __forceinline__ void load_logits(const RouteArgs& p, int64_t t, int e
 // Whether the lane's run of experts is kept.  w: the two best of the lane; a run's worth is off by at
 // most half of `slack`; sure turns false where that could decide.  A run's rank is the number of lanes of
 // runs that are worth more: the 16 lanes of a token are turned around, of 64 one lane of each run is read.
-template <int L>
-__device__ __forceinline__ bool keep_run(const RouteArgs& p, Best2<float> w, int sub, float slack, bool& sure) {
-  auto meet = [&](float a, float b) {
+template <int L, bool EXACT, class S>
+__device__ __forceinline__ bool keep_run(const RouteArgs& p, int lm, Best2<S> w, int sub, S slack, bool& sure) {
+  constexpr S none = -(S)__builtin_inf();
+  auto meet = [&](S a, S b) {
     w.add(a);
     w.add(b);
   };
-  const int lm = p.run_lanes, m = 1 << lm;
+  const int m = 1 << lm;
   if (lm > 0) meet(dpp<0xb1>(w.a), dpp<0xb1>(w.b));    // lanes 1 0 3 2
   if (lm > 1) meet(dpp<0x4e>(w.a), dpp<0x4e>(w.b));    // lanes 2 3 0 1
   if (lm > 2) meet(dpp<0x141>(w.a), dpp<0x141>(w.b));  // eight lanes mirrored: the other four
@@ -329,16 +230,20 @@ __device__ __forceinline__ bool keep_run(const RouteArgs& p, Best2<float> w, int
     if (lm > 4) meet(__shfl_xor(w.a, 16), __shfl_xor(w.b, 16));
     if (lm > 5) meet(__shfl_xor(w.a, 32), __shfl_xor(w.b, 32));
   }
-  const float t = p.group_top == 2 && w.b != kNone ? w.a + w.b : w.a;
+  const S t = p.group_top == 2 && w.b != none ? w.a + w.b : w.a;
   const int first = sub & ~(m - 1);
-  int over = 0, near = 0;  // lanes (of 64: runs) worth more for certain, and those that may be
-  auto rank = [&](float u, int from) {
-    const bool own = ((from ^ sub) & ~(m - 1)) == 0;
-    const bool more = slack == 0.0f && (u > t || (u == t && from < first));
-    over += !own && (slack == 0.0f ? more : u - t > slack);
-    near += !own && (slack == 0.0f ? more : !(t - u > slack));
+  // Lanes (of 64: runs) that are worth more for certain, and those that may be; among the latter the run's
+  // own, which the bound counts too.
+  int over = 0, near = 0, most = p.top_groups;
+  auto rank = [&](S u, int from) {
+    if constexpr (EXACT) {
+      over += u > t || (u == t && from < first);
+    } else {
+      over += u - t > slack;
+      near += !(u - t < -slack);
+    }
   };
-  int most = p.top_groups;
+  int own = 1;
   if constexpr (L == 64) {
     for (int g = 0; g < p.groups; ++g) rank(lane_value(t, g << lm), g << lm);
   } else {
@@ -348,19 +253,128 @@ __device__ __forceinline__ bool keep_run(const RouteArgs& p, Best2<float> w, int
     TGEMM_TURN(11); TGEMM_TURN(12); TGEMM_TURN(13); TGEMM_TURN(14); TGEMM_TURN(15);
 #undef TGEMM_TURN
     most <<= lm;
+    own = m - 1;
   }
-  if (t == kNone) return false;  // no expert there
+  near = EXACT ? over : near - own;
+  if (t == none) return false;  // no expert there
   if (over < most && near >= most) sure = false;
   return near < most;
 }
 
-// choose() in fp32; false in the lanes of a token for which it is not certain.
+// The choice of one token's experts with keys in 64 bits, by a whole wave: lane j gets the j-th (-1: none)
+// and its logit.  x: the lane's logits, -infinity where there is no expert.
+template <int V>
+__device__ __forceinline__ void choose(const RouteArgs& p, const Layout& lay, const float (&x)[V], int lane,
+                                       double rcp_sum, float x_max, int& chosen, float& chosen_x) {
+  constexpr double none = -__builtin_inf();
+  const int e0 = lay.expert<V>(lane), n = lay.count<V>(lane);
+  const bool by_score = !p.bias && p.groups > 1 && p.group_top == 2;
+  double key[V], s[V];
+  if (p.bias || by_score) {
+    if (p.score) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] = 1.0 / (1.0 + exp(-(double)x[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] = exp((double)x[i] - (double)x_max) * rcp_sum;
+    }
+  }
+  if (p.bias) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float b = i < n ? p.bias[e0 + i] : kNone;
+      const double k = s[i] + (double)b;
+      key[i] = x[i] == kNone || b == kNone ? none : k;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = x[i];
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) key[i] = key[i] != key[i] ? -none : key[i];
+  double worth[V];  // of the expert to its run
+#pragma unroll
+  for (int i = 0; i < V; ++i) worth[i] = key[i];
+  if (by_score) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) worth[i] = key[i] == none ? none : s[i] != s[i] ? -none : s[i];
+  }
+  if (lay.runs > 1) {
+    Best2<double> w{none, none};
+#pragma unroll
+    for (int i = 0; i < V; ++i) w.add(worth[i]);
+    bool sure;
+    if (!keep_run<64, true, double>(p, lay.lanes_log2, w, lane, 0.0, sure)) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = none;
+    }
+  } else if (p.groups > 1) {
+    // Runs that do not fit the lanes, one after another: lane h < groups gets what run h is worth.
+    const int size = p.run_size;
+    double total = none;
+    for (int g = 0; g < p.groups; ++g) {
+      Best2<double> m{none, none};
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = e0 + i;
+        m.add(e >= g * size && e < (g + 1) * size ? worth[i] : none);
+      }
+      const double a = max_across<64>(m.a);
+      // the lowest lane that holds it gives up its first
+      const double second = max_across<64>(lane == (int)__builtin_ctzll(__ballot(m.a == a)) ? m.b : m.a);
+      if (g == lane) total = p.group_top == 2 && second != none ? a + second : a;
+    }
+    uint64_t kept = 0;
+    for (int r = 0; r < p.top_groups; ++r) {
+      const double m = max_across<64>(total);
+      if (m == none) break;
+      const int g = (int)__builtin_ctzll(__ballot(total == m));  // the lowest of the runs that are worth it
+      kept |= 1ull << g;
+      if (g == lane) total = none;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (!((kept >> min((e0 + i) / size, 63)) & 1)) key[i] = none;
+  }
+  chosen = -1;
+  chosen_x = 0.0f;
+  for (int j = 0; j < p.top; ++j) {
+    double m = key[0];
+    int at = 0;
+    float xm = x[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i)
+      if (key[i] > m) {
+        m = key[i];
+        at = i;
+        xm = x[i];
+      }
+    const double best = max_across<64>(m);
+    const int first = (int)__builtin_ctzll(__ballot(m == best));
+    const int e = __builtin_amdgcn_readlane(e0 + at, first);
+    const float v = lane_value(xm, first);
+    if (lane == j) {
+      chosen = best == none ? -1 : e;
+      chosen_x = v;
+    }
+    if (lane == first) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i == at) key[i] = none;
+    }
+  }
+}
+
+// ---- the same in fp32, where that is certain ----
+
+// choose() in fp32: lane j of the token's L gets the place (lane * V + i) of the j-th, -1 for none, and its
+// logit; false in the lanes of a token for which fp32 is not enough.
+// logits: the token's in LDS, by place.
 template <int L, int V>
-__device__ __forceinline__ bool choose_quick(const RouteArgs& p, const Layout& lay, const float (&x)[V], int64_t t,
-                                             int lane, int sub, float x_max, float rcp_sum, int& chosen,
-                                             float& chosen_x) {
+__device__ __forceinline__ bool choose_quick(const RouteArgs& p, const Layout& lay, const float (&x)[V],
+                                             const float (&bias)[V], const float* logits, int lane, int sub,
+                                             float x_max, float rcp_sum, int& chosen, float& chosen_x) {
   constexpr uint32_t LOW = V - 1;
-  const int e0 = lay.expert<V>(sub), n = lay.count<V>(sub);
   const bool scored = p.bias || (p.groups > 1 && p.group_top == 2);
   float key[V], s[V];
   float slack = 0.0f;  // bound on the error of a score
@@ -368,108 +382,130 @@ __device__ __forceinline__ bool choose_quick(const RouteArgs& p, const Layout& l
     // Relative errors: the exponential's argument is off by half a step or two of itself, the function
     // and the reciprocal by a step.  z exp(-z) <= 0.37, and z s(-z) falls from z = 1.3 on, so that the
     // argument's part is largest at the largest score.  softmax: its sum is off by up to 10 half steps.
-    float top;
     if (p.score) {
-      top = __builtin_amdgcn_rcpf(1.0f + quick_exp(-x_max));
-      slack = top * (0x1p-21f + fmaxf(1.3f, -x_max) * 0x1p-22f);
-    } else {
-      top = rcp_sum;
-      slack = top * 0x1p-19f;
-    }
+      slack = __builtin_amdgcn_rcpf(1.0f + quick_exp(-x_max)) * (0x1p-21f + fmaxf(1.3f, -x_max) * 0x1p-22f);
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      s[i] = p.score ? __builtin_amdgcn_rcpf(1.0f + quick_exp(-x[i])) : quick_exp(x[i] - x_max) * rcp_sum;
+      for (int i = 0; i < V; ++i) s[i] = __builtin_amdgcn_rcpf(1.0f + quick_exp(-x[i]));
+    } else {
+      slack = rcp_sum * 0x1p-19f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] = quick_exp(x[i] - x_max) * rcp_sum;
+    }
   }
+  constexpr float inf = __builtin_inff();
   if (p.bias) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float b = i < n ? p.bias[e0 + i] : kNone;
-      const float k = s[i] + b;
-      key[i] = x[i] == kNone || b == kNone ? kNone : k != k ? -kNone : k;
+      const float k = fminf(s[i] + bias[i], inf);  // a NaN as infinity
+      key[i] = x[i] == kNone ? kNone : k;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = x[i] != x[i] ? -kNone : x[i];
+    for (int i = 0; i < V; ++i) key[i] = fminf(x[i] + 0.0f, inf);  // (one zero)
   }
   bool sure = true;
+  uint32_t keep = ~LOW;
   if (p.groups > 1) {
     Best2<float> w{kNone, kNone};
-    const bool by_score = !p.bias && p.group_top == 2;
+    if (!p.bias && p.group_top == 2) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float v = by_score && key[i] != kNone ? s[i] : key[i];
-      w.add(v != v ? -kNone : v);
-    }
-    // (a run's sum of two: twice the error, and the rounding of the sum, which is that of the keys too)
-    const float worst = max_across<L>(fmaxf(fabsf(w.a == kNone ? 0.0f : w.a), fabsf(w.b == kNone ? 0.0f : w.b)));
-    const bool exact = !scored;
-    const bool kept = keep_run<L>(p, w, sub, exact ? 0.0f : 4.0f * slack + 0x1p-21f * worst, sure);
-    if (!kept) {
+      for (int i = 0; i < V; ++i) {
+        const float v = fminf(s[i], inf);
+        w.add(key[i] == kNone ? kNone : v);
+      }
+    } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = kNone;
+      for (int i = 0; i < V; ++i) w.add(key[i]);
     }
+    // a run's sum of two: twice the error, and the roundings of the sum and of its keys
+    const float worst = max_across<L>(fmaxf(w.a == kNone ? 0.0f : fabsf(w.a), w.b == kNone ? 0.0f : fabsf(w.b)));
+    const bool kept = scored ? keep_run<L, false, float>(p, lay.lanes_log2, w, sub, 4.0f * slack + 0x1p-21f * worst, sure)
+                             : keep_run<L, true, float>(p, lay.lanes_log2, w, sub, 0.0f, sure);
+    if (!kept) keep = 0u;
   }
+  // (-infinity, and whatever is not kept, is below FINITE)
+  constexpr uint32_t FINITE = 0x00800000u;
   uint32_t u[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    u[i] = key[i] == kNone ? 0u : (ordered(key[i] + 0.0f) & ~LOW) | (LOW - i);  // (+ 0: one zero)
+  for (int i = 0; i < V; ++i) u[i] = (ordered(key[i]) & keep) | (LOW - i);
   sort_falling<V>(u);
-  chosen = -1;
-  uint32_t mine = 0;
   // The best head of the token's lanes, the lowest lane's of equal ones (their last bits are places, not
-  // values), and its expert; it leaves its lane.
-  auto next = [&](int& e) {
+  // values), and its place; it leaves its lane.
+  auto next = [&](int& q) {
     const uint32_t head = u[0] & ~LOW, best = max_across<L>(head);
     const int first = first_lane<L>(head == best, lane);
     const int i = (int)(LOW - (u[0] & LOW));
-    if constexpr (L == 64) e = lay.expert<V>(first) + __builtin_amdgcn_readlane(i, first);
-    else e = lay.expert<V>(first) + (V > 1 ? __shfl(i, (lane & 48) + first) : 0);
+    if constexpr (L == 64) q = first * V + __builtin_amdgcn_readlane(i, first);
+    else q = first * V + (V > 1 ? __shfl(i, (lane & 48) + first) : 0);
     if (sub == first) {
 #pragma unroll
-      for (int q = 0; q + 1 < V; ++q) u[q] = u[q + 1];
+      for (int j = 0; j + 1 < V; ++j) u[j] = u[j + 1];
       u[V - 1] = 0u;
     }
     return best;
   };
-  uint32_t last = 0;
-  int e_last = 0;
-  for (int j = 0; j < p.top; ++j) {
-    last = next(e_last);
-    if (sub == j) {
-      chosen = last ? e_last : -1;
-      mine = last;
-    }
-  }
-  // Is the order certain?  Neighbours of the chosen, in their lanes.
-  const float* const bias = p.bias;
   auto apart = [&](uint32_t a, uint32_t b) {  // a >= b, without their last bits
-    if (!bias) return a != b;  // the logits themselves
+    if (!p.bias) return a != b;  // the logits themselves
     // what the last bits were worth, and two roundings
     const float fa = from_ordered(a), fb = from_ordered(b);
     return fa - fb > 2.0f * slack + (V + 4) * 0x1p-23f * fmaxf(fabsf(fa), fabsf(fb));
   };
-  chosen_x = chosen >= 0 ? load_logit(p.x, t * p.ldx + chosen, p.x_type) : 0.0f;
-  const float b_mine = chosen >= 0 && bias ? bias[chosen] : 0.0f;
-  {
-    const int up = lane + 1;
-    const uint32_t u2 = (uint32_t)__shfl((int)mine, up);
-    const float x2 = __shfl(chosen_x, up), b2 = __shfl(b_mine, up);
-    if (sub + 1 < p.top && u2 && !apart(mine, u2) && !(x2 == chosen_x && b2 == b_mine)) sure = false;
+  uint32_t mine = 0, last = 0;
+  int place = -1;
+  for (int j = 0; j < p.top; ++j) {
+    int q;
+    last = next(q);
+    if (sub == j && last >= FINITE) {
+      mine = last;
+      place = q;
+    }
   }
-  // The last one and those that were not chosen: equal ones may follow (a few are looked at).
-  if (last) {
-    const float xl = load_logit(p.x, t * p.ldx + e_last, p.x_type), bl = bias ? bias[e_last] : 0.0f;
-    for (int more = 0;; ++more) {
-      int e;
-      const uint32_t r = next(e);
-      if (!r || apart(last, r)) break;
-      const bool same = load_logit(p.x, t * p.ldx + e, p.x_type) == xl && (bias ? bias[e] : 0.0f) == bl;
-      if (!same || more == 3) {
+  // Those that were not chosen but may be worth as much as the last one come behind it, up to four.
+  int found = p.top;
+  if (last >= FINITE) {
+    for (;;) {
+      int q;
+      const uint32_t r = next(q);
+      if (r < FINITE || apart(last, r)) break;
+      if (found == (p.top + 4 < L ? p.top + 4 : L)) {
         sure = false;
         break;
       }
+      if (sub == found) {
+        mine = r;
+        place = q;
+      }
+      ++found;
     }
   }
+  // Is the order certain?  Neighbours have to be apart or made of the same numbers.
+  float cx = place >= 0 ? logits[place] : 0.0f;
+  const float cb = p.bias && place >= 0 ? p.bias[lay.of_place<V>(place)] : 0.0f;
+  const uint32_t u2 = (uint32_t)__shfl((int)mine, lane + 1);
+  const bool same = __shfl(cx, lane + 1) == cx && __shfl(cb, lane + 1) == cb;
+  const bool doubt = sub + 1 < found && u2 && !apart(mine, u2) && !same;
+  const uint64_t all = __ballot(doubt);
+  if (L == 64 ? all != 0 : ((all >> (lane & 48)) & 0xffff) != 0) {
+    if (p.bias && !p.score) {
+      sure = false;  // the softmax's sum would be needed in 64 bits
+    } else {
+      // the candidates' keys in 64 bits, and each one's rank among them
+      double k = p.bias ? 1.0 / (1.0 + exp(-(double)cx)) + (double)cb : (double)cx;
+      k = place < 0 ? -__builtin_inf() : k != k ? __builtin_inf() : k;
+      int rank = 0;
+      for (int j = 0; j < found; ++j) {
+        const int from = (lane & ~(L - 1)) + j;
+        const double kj = __shfl(k, from);
+        const int pj = __shfl(place, from);
+        rank += kj > k || (kj == k && (j < sub ? pj <= place : pj < place));
+      }
+      const int to = 4 * ((lane & ~(L - 1)) + (sub < found ? rank : sub));
+      place = __builtin_amdgcn_ds_permute(to, place);
+      cx = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(cx)));
+    }
+  }
+  chosen = sub < p.top ? place : -1;
+  chosen_x = cx;
   return sure;
 }
 
@@ -515,21 +551,20 @@ __device__ __forceinline__ float weight_of(const RouteArgs& p, int chosen, float
 }
 
 // One token again in 64 bits, by the whole wave: lane j < top gets the j-th expert and its logit.
+// run_lanes: the layout's, for VV experts a lane.
 template <int VV>
-__device__ __forceinline__ void choose_again(const RouteArgs& p, int64_t t, int lane, int& chosen, float& cx) {
+__device__ __forceinline__ void choose_again(const RouteArgs& p, int run_lanes, int64_t t, int lane, int& chosen,
+                                             float& cx) {
+  const Layout lay(p, run_lanes);
   float x[VV];
-#pragma unroll
-  for (int i = 0; i < VV; ++i) {
-    const int e = lane * VV + i;
-    x[i] = e < p.E ? load_logit(p.x, t * p.ldx + e, p.x_type) : kNone;
-  }
+  load_logits<VV>(p, t, lay.expert<VV>(lane), lay.count<VV>(lane), x);
   float x_max = 0.0f;
   double sum = 1.0;
   if (!p.score && (p.bias || (p.groups > 1 && p.group_top == 2))) {
     x_max = largest<64, VV>(x);
     sum = softmax_sum<64, VV, double>(x, x_max);
   }
-  choose<64, VV, double>(p, x, lane, lane, 1.0 / sum, x_max, chosen, cx);
+  choose<VV>(p, lay, x, lane, 1.0 / sum, x_max, chosen, cx);
 }
 
 // TB tokens of a workgroup, 64 / L of them to a wave at a time.
@@ -539,20 +574,34 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs p, int TB) {
   __shared__ int start[1024 + 1];
   __shared__ int16_t pick[64 * 32];
   __shared__ int part[THREADS / 64];
+  __shared__ __attribute__((aligned(16))) float logits[THREADS / L][L * V];
   constexpr int VV = (L * V + 63) / 64;
   const int tid = threadIdx.x, lane = tid & 63, sub = lane & (L - 1), wave = tid >> 6, threads = blockDim.x;
   const int64_t t0 = (int64_t)blockIdx.x * TB;
   const int here = (int)min((int64_t)TB, p.T - t0);
+  constexpr int TW = 64 / L;
+  const Layout lay(p, p.run_lanes);
+  const int e0 = lay.expert<V>(sub), n = lay.count<V>(sub);
+  float bias[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) bias[i] = kNone;
+  if (p.bias) {
+    if (n == V) {
+      __builtin_memcpy(bias, p.bias + e0, 4 * V);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < n) bias[i] = p.bias[e0 + i];
+    }
+  }
   for (int e = tid; e < p.E; e += threads) mask[e] = 0ull;
   __syncthreads();
-  constexpr int TW = 64 / L;
-  const Layout lay(p);
   for (int base = wave * TW; base < here; base += threads / 64 * TW) {  // (the same for all lanes of a wave)
     const int local = base + lane / L;
     const bool live = local < here;
     const int64_t t = t0 + (live ? local : here - 1);
     float x[V];
-    load_logits<V>(p, t, lay.expert<V>(sub), lay.count<V>(sub), x);
+    load_logits<V>(p, t, e0, n, x);
     const bool scored = p.bias || (p.groups > 1 && p.group_top == 2);
     float x_max = 0.0f, sum = 1.0f;
     if (scored || (!p.score && !p.renorm)) {
@@ -562,14 +611,26 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs p, int TB) {
     int chosen = -1;
     float cx = 0.0f;
     bool sure = false;
-    if (p.run_lanes >= 0) sure = choose_quick<L, V>(p, lay, x, t, lane, sub, x_max, 1.0f / sum, chosen, cx);
+    if (p.run_lanes >= 0) {
+      // the wave's own rows: its writes and reads of them keep their order
+      float* const row = logits[tid / L];
+#pragma unroll
+      for (int i = 0; i < V; ++i) row[sub * V + i] = x[i];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      int place;
+      sure = choose_quick<L, V>(p, lay, x, bias, row, lane, sub, x_max, 1.0f / sum, place, cx);
+      chosen = place >= 0 ? lay.of_place<V>(place) : -1;
+    }
     for (uint64_t again = __ballot(!sure); again;) {
       const int from = (int)__builtin_ctzll(again) & ~(L - 1);  // the token's first lane
       again &= ~((L == 64 ? ~0ull : 0xffffull) << from);
       const int at = base + from / L;
       int c;
       float v;
-      choose_again<VV>(p, t0 + (at < here ? at : here - 1), lane, c, v);
+      // (a quarter of the experts to a lane, so four times the lanes to a run)
+      choose_again<VV>(p, p.run_lanes < 0 || L == 64 || V == 1 ? p.run_lanes : p.run_lanes + 2,
+                       t0 + (at < here ? at : here - 1), lane, c, v);
       const int cs = __shfl(c, sub);
       const float vs = __shfl(v, sub);
       if ((lane & ~(L - 1)) == from) {
@@ -593,11 +654,7 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs p, int TB) {
       const int e = base + tid;
       int v = e < p.E ? __popcll(mask[e]) : 0;
       const int own = v;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int u = __shfl_up(v, d);
-        if (lane >= d) v += u;
-      }
+      v = scan_add(v);
       if (lane == 63) part[wave] = v;
       __syncthreads();
       int before = carry, all = 0;
@@ -618,7 +675,7 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs p, int TB) {
     for (int e = tid; e < route_row_bytes(p.E); e += threads) row[e] = e < p.E ? (uint8_t)__popcll(mask[e]) : 0;
   }
   for (int i = tid; i < here * p.top; i += threads) {
-    const int e = pick[i], local = i / p.top;
+    const int e = pick[i], local = (int)((uint32_t)(i * p.per_top) >> 16);
     int at = -1;
     if (e >= 0) at = __popcll(mask[e] & ((1ull << local) - 1)) + (p.ws ? 0 : start[e]);
     p.place[t0 * p.top + i] = at;
@@ -684,11 +741,7 @@ __global__ __launch_bounds__(256) void route_place_kernel(RouteArgs p, int TB, i
     const int e = base + tid;
     int v = e < p.E ? total[e] : 0;
     const int own = v;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int u = __shfl_up(v, d);
-      if (lane >= d) v += u;
-    }
+    v = scan_add(v);
     if (lane == 63) part[wave] = v;
     __syncthreads();
     int b = carry, all = 0;
@@ -824,6 +877,8 @@ hipError_t route_launch(const RouteArgs& p, int TB, hipStream_t s) {
 
 hipError_t launch_route(const RouteArgs& args, hipStream_t s) {
   RouteArgs p = args;
+  p.run_size = p.E / p.groups;
+  p.per_top = (65536 + p.top - 1) / p.top;
   const int TB = route_block_tokens(p.T);
   // Lanes of a token: 16 hold a choice of at most 16; a few tokens are over sooner with 64 lanes each, and
   // so many experts do not fit 16.  Experts of a lane: the fewest that hold all of them, runs of them in
@@ -833,7 +888,7 @@ hipError_t launch_route(const RouteArgs& args, hipStream_t s) {
       p.run_lanes = 6;
       return p.E <= L * V;
     }
-    const int size = p.E / p.groups;
+    const int size = p.run_size;
     p.run_lanes = 0;
     while ((V << p.run_lanes) < size) ++p.run_lanes;
     return p.groups << p.run_lanes <= L;
@@ -848,7 +903,7 @@ hipError_t launch_route(const RouteArgs& args, hipStream_t s) {
     e = fits(16, 1)   ? route_launch<16, 1, 1024>(p, TB, s)
         : fits(16, 4) ? route_launch<16, 4, 1024>(p, TB, s)
         : fits(16, 8) ? route_launch<16, 8, 1024>(p, TB, s)
-                      : (fits(16, 16), route_launch<16, 16, 1024>(p, TB, s));
+                      : (fits(16, 16), route_launch<16, 16, 512>(p, TB, s));
   const bool one = p.T <= 64;
   if (e != hipSuccess || one) return e;
   const int64_t blocks = route_blocks(p.T);

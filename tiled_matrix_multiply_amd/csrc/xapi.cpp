@@ -304,7 +304,7 @@ gemm_status_t gemm_route(gemm_handle_t h, void* stream, int64_t tokens, int64_t 
   if (st != GEMM_OK) return st;
   const tgemm::RouteArgs p{logits, ldl, (int)tokens, (int)experts, (int)top, (int)x_type, (int)score, bias, (int)groups,
                            (int)top_groups, group_top, renorm, scale, expert, weight, place, offsets,
-                           tokens <= 64 ? nullptr : static_cast<uint8_t*>(workspace), 0};
+                           tokens <= 64 ? nullptr : static_cast<uint8_t*>(workspace), 0, 0, 0};
   tgemm::DeviceGuard g(h->device);
   return status(tgemm::launch_route(p, static_cast<hipStream_t>(stream)));
 }
