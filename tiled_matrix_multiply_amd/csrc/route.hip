@@ -212,8 +212,8 @@ __device__ __forceinline__ void load_logits(const RouteArgs& p, int64_t t, int e
 }
 
 // Whether the lane's run of experts is kept.  w: the two best of the lane; a run's worth is off by at
-// most half of `slack`; sure turns false where that could decide.  A run's rank is the number of lanes of
-// runs that are worth more: the 16 lanes of a token are turned around, of 64 one lane of each run is read.
+// most half of `slack`; sure turns false where that could decide.  A run's rank is the number of runs that
+// are worth more: the 16 lanes of a token are turned by its length, of 64 one lane of each run is read.
 template <int L, bool EXACT, class S>
 __device__ __forceinline__ bool keep_run(const RouteArgs& p, int lm, Best2<S> w, int sub, S slack, bool& sure) {
   constexpr S none = -(S)__builtin_inf();
@@ -232,9 +232,7 @@ __device__ __forceinline__ bool keep_run(const RouteArgs& p, int lm, Best2<S> w,
   }
   const S t = p.group_top == 2 && w.b != none ? w.a + w.b : w.a;
   const int first = sub & ~(m - 1);
-  // Lanes (of 64: runs) that are worth more for certain, and those that may be; among the latter the run's
-  // own, which the bound counts too.
-  int over = 0, near = 0, most = p.top_groups;
+  int over = 0, near = 0;  // runs that are worth more for certain, and those that may be
   auto rank = [&](S u, int from) {
     if constexpr (EXACT) {
       over += u > t || (u == t && from < first);
@@ -243,22 +241,27 @@ __device__ __forceinline__ bool keep_run(const RouteArgs& p, int lm, Best2<S> w,
       near += !(u - t < -slack);
     }
   };
-  int own = 1;
   if constexpr (L == 64) {
     for (int g = 0; g < p.groups; ++g) rank(lane_value(t, g << lm), g << lm);
+    near -= 1;  // (its own)
   } else {
 #define TGEMM_TURN(r) rank(dpp<0x120 + r>(t), (sub - r) & 15)
-    TGEMM_TURN(1); TGEMM_TURN(2); TGEMM_TURN(3); TGEMM_TURN(4); TGEMM_TURN(5);
-    TGEMM_TURN(6); TGEMM_TURN(7); TGEMM_TURN(8); TGEMM_TURN(9); TGEMM_TURN(10);
-    TGEMM_TURN(11); TGEMM_TURN(12); TGEMM_TURN(13); TGEMM_TURN(14); TGEMM_TURN(15);
+    if (lm < 1) {
+      TGEMM_TURN(1); TGEMM_TURN(3); TGEMM_TURN(5); TGEMM_TURN(7); TGEMM_TURN(9); TGEMM_TURN(11); TGEMM_TURN(13); TGEMM_TURN(15);
+    }
+    if (lm < 2) {
+      TGEMM_TURN(2); TGEMM_TURN(6); TGEMM_TURN(10); TGEMM_TURN(14);
+    }
+    if (lm < 3) {
+      TGEMM_TURN(4); TGEMM_TURN(12);
+    }
+    if (lm < 4) TGEMM_TURN(8);
 #undef TGEMM_TURN
-    most <<= lm;
-    own = m - 1;
   }
-  near = EXACT ? over : near - own;
+  if (EXACT) near = over;
   if (t == none) return false;  // no expert there
-  if (over < most && near >= most) sure = false;
-  return near < most;
+  if (over < p.top_groups && near >= p.top_groups) sure = false;
+  return near < p.top_groups;
 }
 
 // The choice of one token's experts with keys in 64 bits, by a whole wave: lane j gets the j-th (-1: none)
@@ -369,10 +372,12 @@ __device__ __forceinline__ void choose(const RouteArgs& p, const Layout& lay, co
 
 // choose() in fp32: lane j of the token's L gets the place (lane * V + i) of the j-th, -1 for none, and its
 // logit; false in the lanes of a token for which fp32 is not enough.
-// logits: the token's in LDS, by place.
+// logits: the token's in LDS, by place, and biases alike; record: L + 1 of the token's own in LDS.
+typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
 template <int L, int V>
 __device__ __forceinline__ bool choose_quick(const RouteArgs& p, const Layout& lay, const float (&x)[V],
-                                             const float (&bias)[V], const float* logits, int lane, int sub,
+                                             const float (&bias)[V], const float* logits,
+                                             const float* biases, u2_t* record, int lane, int sub,
                                              float x_max, float rcp_sum, int& chosen, float& chosen_x) {
   constexpr uint32_t LOW = V - 1;
   const bool scored = p.bias || (p.groups > 1 && p.group_top == 2);
@@ -430,18 +435,14 @@ __device__ __forceinline__ bool choose_quick(const RouteArgs& p, const Layout& l
   for (int i = 0; i < V; ++i) u[i] = (ordered(key[i]) & keep) | (LOW - i);
   sort_falling<V>(u);
   // The best head of the token's lanes, the lowest lane's of equal ones (their last bits are places, not
-  // values), and its place; it leaves its lane.
-  auto next = [&](int& q) {
+  // values), becomes the token's j-th record and leaves its lane.
+  auto next = [&](int j) {
     const uint32_t head = u[0] & ~LOW, best = max_across<L>(head);
-    const int first = first_lane<L>(head == best, lane);
-    const int i = (int)(LOW - (u[0] & LOW));
-    if constexpr (L == 64) q = first * V + __builtin_amdgcn_readlane(i, first);
-    else q = first * V + (V > 1 ? __shfl(i, (lane & 48) + first) : 0);
-    if (sub == first) {
+    const bool own = sub == first_lane<L>(head == best, lane);
+    if (own) record[j] = u2_t{best, (uint32_t)(sub * V) + LOW - (u[0] & LOW)};
+    // (selects: moves inside the branch cost the loop twice as many instructions)
 #pragma unroll
-      for (int j = 0; j + 1 < V; ++j) u[j] = u[j + 1];
-      u[V - 1] = 0u;
-    }
+    for (int i = 0; i < V; ++i) u[i] = own ? (i + 1 < V ? u[i + 1 < V ? i + 1 : i] : 0u) : u[i];
     return best;
   };
   auto apart = [&](uint32_t a, uint32_t b) {  // a >= b, without their last bits
@@ -450,37 +451,30 @@ __device__ __forceinline__ bool choose_quick(const RouteArgs& p, const Layout& l
     const float fa = from_ordered(a), fb = from_ordered(b);
     return fa - fb > 2.0f * slack + (V + 4) * 0x1p-23f * fmaxf(fabsf(fa), fabsf(fb));
   };
-  uint32_t mine = 0, last = 0;
-  int place = -1;
-  for (int j = 0; j < p.top; ++j) {
-    int q;
-    last = next(q);
-    if (sub == j && last >= FINITE) {
-      mine = last;
-      place = q;
-    }
-  }
+  uint32_t last = 0;
+  for (int j = 0; j < p.top; ++j) last = next(j);
   // Those that were not chosen but may be worth as much as the last one come behind it, up to four.
   int found = p.top;
   if (last >= FINITE) {
+    const int most = p.top + 4 < L ? p.top + 4 : L;
     for (;;) {
-      int q;
-      const uint32_t r = next(q);
+      const uint32_t r = next(found);
       if (r < FINITE || apart(last, r)) break;
-      if (found == (p.top + 4 < L ? p.top + 4 : L)) {
+      if (++found > most) {
         sure = false;
         break;
       }
-      if (sub == found) {
-        mine = r;
-        place = q;
-      }
-      ++found;
     }
   }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  const u2_t got = record[sub < found ? sub : 0];
+  const bool there = sub < found && got[0] >= FINITE;
+  const uint32_t mine = there ? got[0] : 0u;
+  int place = there ? (int)got[1] : -1;
   // Is the order certain?  Neighbours have to be apart or made of the same numbers.
   float cx = place >= 0 ? logits[place] : 0.0f;
-  const float cb = p.bias && place >= 0 ? p.bias[lay.of_place<V>(place)] : 0.0f;
+  const float cb = p.bias && place >= 0 ? biases[place] : 0.0f;
   const uint32_t u2 = (uint32_t)__shfl((int)mine, lane + 1);
   const bool same = __shfl(cx, lane + 1) == cx && __shfl(cb, lane + 1) == cb;
   const bool doubt = sub + 1 < found && u2 && !apart(mine, u2) && !same;
@@ -532,12 +526,20 @@ __device__ __forceinline__ S softmax_sum(const float (&x)[V], float x_max) {
   }
 }
 
+// exp(v) within two steps: the product with log2(e) in two parts.
+__device__ __forceinline__ float exp_near(float v) {
+  constexpr float hi = 1.44269502f, lo = 1.92596299e-8f;  // log2(e) in two fp32 numbers
+  const float t = v * hi, rest = fmaf(v, lo, fmaf(v, hi, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return fabsf(v) < 80.0f ? fmaf(e, rest * 0.693147181f, e) : e;  // (past that e or the rest may be no number)
+}
+
 // Weight of the lane's chosen expert among the token's: p.top lanes hold one each.
 template <int L, int V>
 __device__ __forceinline__ float weight_of(const RouteArgs& p, int chosen, float cx, float x_max, float sum) {
   const bool there = chosen >= 0;
   if (!p.renorm) {
-    const float s = p.score ? 1.0f / (1.0f + expf(-cx)) : expf(cx - x_max) / sum;
+    const float s = p.score ? __builtin_amdgcn_rcpf(1.0f + exp_near(-cx)) : exp_near(cx - x_max) / sum;
     return there ? p.scale * s : 0.0f;
   }
   // Relative to the largest chosen logit, so that the sum is at least 1/2: exp(x - m) for softmax; for
@@ -545,7 +547,14 @@ __device__ __forceinline__ float weight_of(const RouteArgs& p, int chosen, float
   const float top = max_across<L>(there ? (cx != cx ? __builtin_inff() : cx) : kNone);
   const float m = p.score ? fminf(top, 0.0f) : top;
   float s = 0.0f;
-  if (there) s = !p.score ? expf(cx - m) : cx > 0.0f ? 1.0f / (1.0f + expf(-cx)) : expf(cx - m) / (1.0f + expf(cx));
+  if (p.score) {
+    // x > 0: then m = 0 and the score is 1 / (1 + exp(-x))
+    const float e = exp_near(cx > 0.0f ? -cx : cx);
+    s = (cx > 0.0f ? 1.0f : exp_near(cx - m)) * __builtin_amdgcn_rcpf(1.0f + e);
+  } else {
+    s = exp_near(cx - m);
+  }
+  if (!there) s = 0.0f;
   const float all = sum_across<L>(s);
   return there ? p.scale * (s / all) : 0.0f;
 }
@@ -575,6 +584,8 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs p, int TB) {
   __shared__ int16_t pick[64 * 32];
   __shared__ int part[THREADS / 64];
   __shared__ __attribute__((aligned(16))) float logits[THREADS / L][L * V];
+  __shared__ __attribute__((aligned(16))) float biases[L * V];
+  __shared__ u2_t record[THREADS / L][L + 1];
   constexpr int VV = (L * V + 63) / 64;
   const int tid = threadIdx.x, lane = tid & 63, sub = lane & (L - 1), wave = tid >> 6, threads = blockDim.x;
   const int64_t t0 = (int64_t)blockIdx.x * TB;
@@ -593,6 +604,10 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs p, int TB) {
       for (int i = 0; i < V; ++i)
         if (i < n) bias[i] = p.bias[e0 + i];
     }
+  }
+  if (tid < L) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) biases[sub * V + i] = bias[i];
   }
   for (int e = tid; e < p.E; e += threads) mask[e] = 0ull;
   __syncthreads();
@@ -619,7 +634,7 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs p, int TB) {
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
       int place;
-      sure = choose_quick<L, V>(p, lay, x, bias, row, lane, sub, x_max, 1.0f / sum, place, cx);
+      sure = choose_quick<L, V>(p, lay, x, bias, row, biases, record[tid / L], lane, sub, x_max, 1.0f / sum, place, cx);
       chosen = place >= 0 ? lay.of_place<V>(place) : -1;
     }
     for (uint64_t again = __ballot(!sure); again;) {
@@ -683,65 +698,64 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs p, int TB) {
 }
 
 // The second kernel: places within a block become places in the whole.  Every workgroup adds up the
-// table of counts, all blocks' and those before its own (the table is read from the L2).
+// table of counts, all blocks' and those before its own (the table is read from the L2), 4 experts to a
+// thread: bytes apart in sums of 16 bits, flushed before they could pass 65535 (1000 rows of at most 64).
 __global__ __launch_bounds__(256) void route_place_kernel(RouteArgs p, int TB, int blocks) {
   __shared__ int total[1024], before[1024], start[1024];
   __shared__ int part[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int b0 = (int)((int64_t)blockIdx.x * blocks / gridDim.x), b1 = (int)((int64_t)(blockIdx.x + 1) * blocks / gridDim.x);
+  // the first block's pairs, fetched while the table is
+  constexpr int AHEAD = 2;
+  const int64_t at0 = (int64_t)b0 * TB * p.top;
+  const int pairs0 = (int)min((int64_t)TB, p.T - (int64_t)b0 * TB) * p.top;
+  int e_first[AHEAD], rank_first[AHEAD];
+#pragma unroll
+  for (int q = 0; q < AHEAD; ++q) {
+    const int i = min(tid + 256 * q, pairs0 - 1);
+    e_first[q] = p.expert[at0 + i];
+    rank_first[q] = p.place[at0 + i];
+  }
   for (int e = tid; e < 1024; e += 256) total[e] = before[e] = 0;
   __syncthreads();
   const int64_t row = route_row_bytes(p.E);
-  const int per = (int)(row / 16);  // 16 experts to a thread
-  const int rows = 256 / per, c = tid % per, r = tid / per;
+  const int per = (int)(row / 4), rows = 256 / per, c = tid % per, r = tid / per;
   if (r < rows) {
-    // 16 counts of a row in four words, taken apart into sums of 16 bits each (flushed before they could
-    // pass 65535: 1000 rows of at most 64); eight loads in flight
-    auto flush = [&](uint32_t (&w)[8], int* to) {
+    const uint8_t* const table = p.ws + 4 * c;
+    auto add_up = [&](int from, int to, int* sums, int* more) {  // blocks from, from + rows, .. below to
+      for (int chunk = from; chunk < to; chunk += 1000 * rows) {
+        const int end = (int)min((int64_t)to, (int64_t)chunk + 1000 * rows);
+        uint32_t even = 0, odd = 0;
+        for (int b = chunk; b < end; b += 16 * rows) {
+          uint32_t v[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = 16 * c + 4 * (i / 2) + (i & 1);  // even words: bytes 0 and 2, odd: 1 and 3
-        atomicAdd(&to[e], (int)(w[i] & 0xffffu));
-        atomicAdd(&to[e + 2], (int)(w[i] >> 16));
-        w[i] = 0;
-      }
-    };
-    uint32_t all[8] = {}, mine[8] = {};
-    int held = 0;
-    for (int b = r; b < blocks; b += 8 * rows) {
-      r_u32x4 v[8];
+          for (int q = 0; q < 16; ++q) {
+            const int64_t at = min(b + (int64_t)q * rows, (int64_t)end - 1);
+            v[q] = *reinterpret_cast<const uint32_t*>(table + at * row);
+          }
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        __builtin_memcpy(&v[q], p.ws + min(b + q * rows, blocks - 1) * row + 16 * c, 16);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int at = b + q * rows;
-        const uint32_t in = at < blocks ? 0x00ff00ffu : 0u, below = at < b0 ? 0x00ff00ffu : 0u;
+          for (int q = 0; q < 16; ++q) {
+            const uint32_t w = b + (int64_t)q * rows < end ? v[q] : 0u;
+            even += w & 0x00ff00ffu;
+            odd += (w >> 8) & 0x00ff00ffu;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          all[2 * i] += v[q][i] & in;
-          all[2 * i + 1] += (v[q][i] >> 8) & in;
-          mine[2 * i] += v[q][i] & below;
-          mine[2 * i + 1] += (v[q][i] >> 8) & below;
+          const int n = (int)(((i & 1 ? odd : even) >> (8 * (i & 2))) & 0xffffu);
+          atomicAdd(&sums[4 * c + i], n);
+          if (more) atomicAdd(&more[4 * c + i], n);
         }
       }
-      held += 8;
-      if (held >= 1000) {
-        flush(all, total);
-        flush(mine, before);
-        held = 0;
-      }
-    }
-    flush(all, total);
-    flush(mine, before);
+    };
+    add_up(r, b0, total, before);
+    add_up(b0 + ((r - b0) % rows + rows) % rows, blocks, total, nullptr);
   }
   __syncthreads();
   int carry = 0;
   for (int base = 0; base < p.E; base += 256) {
     const int e = base + tid;
-    int v = e < p.E ? total[e] : 0;
-    const int own = v;
-    v = scan_add(v);
+    const int own = e < p.E ? total[e] : 0, v = scan_add(own);
     if (lane == 63) part[wave] = v;
     __syncthreads();
     int b = carry, all = 0;
@@ -760,11 +774,19 @@ __global__ __launch_bounds__(256) void route_place_kernel(RouteArgs p, int TB, i
   for (int b = b0; b < b1; ++b) {
     const int64_t t0 = (int64_t)b * TB;
     const int n = (int)min((int64_t)TB, p.T - t0) * p.top;
-    for (int i = tid; i < n; i += 256) {
+    int done = 0;
+    if (b == b0) {
+#pragma unroll
+      for (int q = 0; q < AHEAD; ++q)
+        if (tid + 256 * q < n && e_first[q] >= 0) p.place[at0 + tid + 256 * q] = rank_first[q] + start[e_first[q]];
+      done = 256 * AHEAD;
+    }
+    for (int i = done + tid; i < n; i += 256) {
       const int64_t at = t0 * p.top + i;
       const int e = p.expert[at];
       if (e >= 0) p.place[at] += start[e];
     }
+    if (b + 1 == b1) break;
     __syncthreads();
     for (int e = tid; e < p.E; e += 256) start[e] += p.ws[b * row + e];
     __syncthreads();
