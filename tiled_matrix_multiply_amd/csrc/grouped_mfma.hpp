@@ -293,27 +293,37 @@ hipError_t launch_rows_type(const GemmParams& p, const GroupArgs& ga, bool b_mn,
   return b_mn ? launch_rows_layout<DT, CT, true>(p, ga, tile, cus, s) : launch_rows_layout<DT, CT, false>(p, ga, tile, cus, s);
 }
 
-// The same tiles in MXFP4 (both operands packed along K; K, lda and ldb in bytes).  Their block scales are
-// staged beside the data for two K tiles at a time, which leaves the 128 x 128 tile three stages; K is
-// not split.
+// The same tiles in MXFP4 (both operands packed along K; K, lda and ldb in bytes; K is not split).  Their
+// block scales are staged beside the data for two K tiles at a time.
+//  * 64 x 64: at the rate of the memory with few rows to a group (64 rows over 32 groups of 2048 x 2048 14 us,
+//    71 MB; streamed 18); deep, three stages instead of two, for few tiles of a long K (16 x 28672 x 8192 31
+//    us against 35, but 384 x 4096 x 4096 13.7 against 13.1);
+//  * 128 x 128: four waves and two stages, so that two workgroups share a compute unit and one's products
+//    hide the other's copies and output (4096 rows over 32 groups of 2048 x 2048 24 us; eight waves with
+//    three stages, as the mixed kernel has to have them, 30).
 template <int CT, int TILE> struct GroupedMxCfg;
 template <int CT> struct GroupedMxCfg<CT, GT_64> {
   using T = MfmaCfg<E2M1, 64, 2, 2, false, false, 2, E2M1, true, 0, 1, 0, 1, CT, true>;
 };
+template <int CT> struct GroupedMxCfg<CT, GT_64_DEEP> {
+  using T = MfmaCfg<E2M1, 64, 2, 2, false, false, 3, E2M1, true, 0, 1, 0, 1, CT, true>;
+};
 template <int CT> struct GroupedMxCfg<CT, GT_128> {
-  using T = MfmaCfg<E2M1, 128, 2, 4, false, false, 3, E2M1, true, 0, 1, 0, 1, CT, true>;
+  using T = MfmaCfg<E2M1, 128, 2, 2, false, false, 2, E2M1, true, 0, 1, 0, 1, CT, true>;
 };
 template <int CT> struct GroupedMxCfg<CT, GT_256> {
   using T = MfmaCfg<E2M1, 256, 2, 4, false, false, 2, E2M1, true, 0, 1, 0, 1, CT, true>;
+  using Small = MfmaCfg<E2M1, 128, 2, 4, false, false, 3, E2M1, true, 0, 1, 0, 1, CT, true>;
 };
 
 template <int CT>
 hipError_t launch_mx_type(const GemmParams& p, const GroupArgs& ga, int tile, int cus, hipStream_t s) {
+  using Large = GroupedMxCfg<CT, GT_256>;
   switch (tile) {
     case GT_64: return launch_rows_cfg<typename GroupedMxCfg<CT, GT_64>::T>(p, ga, s);
+    case GT_64_DEEP: return launch_rows_cfg<typename GroupedMxCfg<CT, GT_64_DEEP>::T>(p, ga, s);
     case GT_128: return launch_rows_cfg<typename GroupedMxCfg<CT, GT_128>::T>(p, ga, s);
-    case GT_256:
-      return launch_mixed_cfg<typename GroupedMxCfg<CT, GT_256>::T, typename GroupedMxCfg<CT, GT_128>::T>(p, ga, cus, s);
+    case GT_256: return launch_mixed_cfg<typename Large::T, typename Large::Small>(p, ga, cus, s);
     default: return hipErrorInvalidValue;
   }
 }

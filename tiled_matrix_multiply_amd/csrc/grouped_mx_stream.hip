@@ -1,9 +1,9 @@
 // Products by expert in MXFP4 for few rows per group (decoding), where the weights are read once and
 // nothing else matters; and for any alignment (gfx950 only).
 //
-// As the streaming kernel of the wider types: a workgroup owns 32 columns of one group and up to 16 MF
-// of its rows, its waves share out K and meet in LDS at the end, in wave order, and weights and rows go
-// straight from global memory into the registers of scaled 16 x 16 x 128 matrix instructions.  Lane l
+// As the streaming kernel of the wider types: a workgroup owns 16 NF columns of one group and up to 16 MF
+// of its rows, its four waves share out K and meet in LDS at the end, in wave order, and weights and rows
+// go straight from global memory into the registers of scaled 16 x 16 x 128 matrix instructions.  Lane l
 // of a fragment holds row (column) l % 16 and the 32 elements k = 32 (l / 16) .. + 31 of a step of 128, 16
 // bytes, with the one scale that belongs to them.  A unit is U steps; its 4 U scale bytes of a row come
 // in one load, the same for the four lanes of the row, and each lane moves its own byte of a step down.
@@ -19,7 +19,7 @@ typedef float x_f32x4 __attribute__((ext_vector_type(4)));
 typedef int x_i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t x_u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int NF = 2, BN = 16 * NF;  // fragments and columns of a workgroup
+constexpr int NW = 4;  // waves of a workgroup
 
 __device__ __forceinline__ x_f32x4 mma_mx(x_u32x4 x, x_u32x4 y, x_f32x4 c, int sx, int sy) {
   const x_i32x8 a = x_i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
@@ -28,11 +28,11 @@ __device__ __forceinline__ x_f32x4 mma_mx(x_u32x4 x, x_u32x4 y, x_f32x4 c, int s
 }
 
 // K and the leading dimensions of A and B are in bytes (two elements each).
-template <int MF, int U>
-__global__ __launch_bounds__(512) void mx_stream_kernel(GemmParams p, GroupArgs ga, int c_type) {
-  constexpr int BM = 16 * MF, PART = NF * MF * 64 * 16;
-  extern __shared__ __attribute__((aligned(16))) uint8_t part[];
-  const int lane = threadIdx.x & 63, NW = blockDim.x >> 6;
+template <int NF, int MF, int U>
+__global__ __launch_bounds__(64 * NW) void mx_stream_kernel(GemmParams p, GroupArgs ga, int c_type) {
+  constexpr int BM = 16 * MF, BN = 16 * NF;
+  __shared__ x_f32x4 part[NW][NF * MF][64];
+  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const GroupItem it = group_item(ga, p.M, BM, p.tiles_n, workgroup(ga), lane);
   if (it.group < 0) return;
@@ -150,17 +150,16 @@ __global__ __launch_bounds__(512) void mx_stream_kernel(GemmParams p, GroupArgs 
     }
   }
 
-  x_f32x4* const mine = reinterpret_cast<x_f32x4*>(part + wave * PART);
 #pragma unroll
   for (int j = 0; j < NF; ++j)
 #pragma unroll
-    for (int f = 0; f < MF; ++f) mine[(j * MF + f) * 64 + lane] = acc[j][f];
+    for (int f = 0; f < MF; ++f) part[wave][j * MF + f][lane] = acc[j][f];
   __syncthreads();
 
   // A lane of fragment (j, f) holds row 16 f + l16 and, in register r, column 16 j + 4 q + r.
   auto finish = [&](auto ct) {
     constexpr int CT = decltype(ct)::value;
-    for (int i = threadIdx.x; i < NF * MF * 64; i += blockDim.x) {
+    for (int i = threadIdx.x; i < NF * MF * 64; i += 64 * NW) {
       const int l = i & 63, jf = i >> 6;
       const int m = m0 + 16 * (jf % MF) + (l & 15), n = n0 + 16 * (jf / MF) + 4 * (l >> 4);
       if (m >= p.M || n >= p.N) continue;
@@ -172,7 +171,8 @@ __global__ __launch_bounds__(512) void mx_stream_kernel(GemmParams p, GroupArgs 
         cin[e] = p.beta != 0.0f ? load_as_float<CT>(p.C, (int64_t)m * p.ldc + col) : 0.0f;
       }
       x_f32x4 v = x_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      for (int w = 0; w < NW; ++w) v += reinterpret_cast<const x_f32x4*>(part + w * PART)[jf * 64 + l];
+#pragma unroll
+      for (int w = 0; w < NW; ++w) v += part[w][jf][l];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (n + e < p.N)
@@ -184,25 +184,26 @@ __global__ __launch_bounds__(512) void mx_stream_kernel(GemmParams p, GroupArgs 
   else finish(std::integral_constant<int, BF16>{});
 }
 
-template <int MF, int U>
-hipError_t launch_cfg(GemmParams p, GroupArgs ga, int c_type, int waves, hipStream_t s) {
-  p.tiles_n = (p.N + BN - 1) / BN;
+template <int NF, int MF, int U>
+hipError_t launch_cfg(GemmParams p, GroupArgs ga, int c_type, hipStream_t s) {
+  p.tiles_n = (p.N + 16 * NF - 1) / (16 * NF);
   const int64_t grid = whole_rounds(max_row_tiles(p.M, ga.groups, 16 * MF) * p.tiles_n);
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  return launch_in_slices(grid, 64 * waves, [&](int64_t first, unsigned n) {
+  return launch_in_slices(grid, 64 * NW, [&](int64_t first, unsigned n) {
     ga.first = (int)first;
-    hipLaunchKernelGGL((mx_stream_kernel<MF, U>), dim3(n), dim3(64 * waves), waves * NF * MF * 64 * 16, s, p, ga, c_type);
+    hipLaunchKernelGGL((mx_stream_kernel<NF, MF, U>), dim3(n), dim3(64 * NW), 0, s, p, ga, c_type);
   });
 }
 
 }  // namespace
 
-// rows: 16, 32 or 64 rows of C per workgroup.
-hipError_t launch_stream_mx(const GemmParams& p, const GroupArgs& ga, int c_type, int rows, int waves, hipStream_t s) {
+// rows: 16, 32 or 64 rows of C per workgroup; columns: 16 (with 16 rows only) or 32.
+hipError_t launch_stream_mx(const GemmParams& p, const GroupArgs& ga, int c_type, int rows, int columns, hipStream_t s) {
+  if (columns == 16) return rows == 16 ? launch_cfg<1, 1, 4>(p, ga, c_type, s) : hipErrorInvalidValue;
   switch (rows) {
-    case 16: return launch_cfg<1, 4>(p, ga, c_type, waves, s);
-    case 32: return launch_cfg<2, 2>(p, ga, c_type, waves, s);
-    case 64: return launch_cfg<4, 2>(p, ga, c_type, waves, s);
+    case 16: return launch_cfg<2, 1, 4>(p, ga, c_type, s);
+    case 32: return launch_cfg<2, 2, 2>(p, ga, c_type, s);
+    case 64: return launch_cfg<2, 4, 2>(p, ga, c_type, s);
     default: return hipErrorInvalidValue;
   }
 }

@@ -12,8 +12,6 @@ namespace {
 
 typedef uint32_t z_u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int UNROLL = 4;  // groups of 512 elements a wave takes of a row together
-
 // 8 elements of a row from element k on (k + 8 <= K: K is a multiple of 32), any alignment.
 template <int XT>
 __device__ __forceinline__ void load8(const uint8_t* row, int64_t k, float (&x)[8]) {
@@ -33,7 +31,8 @@ __device__ __forceinline__ void load8(const uint8_t* row, int64_t k, float (&x)[
   }
 }
 
-template <int XT>
+// UNROLL: groups of 512 elements a wave takes of a row together.
+template <int XT, int UNROLL>
 __global__ __launch_bounds__(256) void quantize_mx_kernel(QuantizeMxArgs p, int64_t first, int per) {
   constexpr int ES = DTypeInfo<XT>::bytes;
   const int lane = threadIdx.x & 63;
@@ -91,15 +90,30 @@ __global__ __launch_bounds__(256) void quantize_mx_kernel(QuantizeMxArgs p, int6
   }
 }
 
+template <int XT, int UNROLL>
+hipError_t launch_unroll(const QuantizeMxArgs& p, hipStream_t s) {
+  const int64_t per = ((int64_t)p.K + 512 * UNROLL - 1) / (512 * UNROLL);
+  return launch_in_slices((p.M * per + 3) / 4, 256, [&](int64_t first, unsigned n) {
+    hipLaunchKernelGGL((quantize_mx_kernel<XT, UNROLL>), dim3(n), dim3(256), 0, s, p, first, (int)per);
+  });
+}
+
+// Four groups a wave keep four loads in flight; a small matrix spreads over more waves instead (1 x 8192
+// 4.0 us against 4.7, 37 x 4128 2.9 against 3.8).
+template <int XT>
+hipError_t launch_type(const QuantizeMxArgs& p, hipStream_t s) {
+  return (int64_t)p.M * p.K <= 512 * 4096 ? launch_unroll<XT, 1>(p, s) : launch_unroll<XT, 4>(p, s);
+}
+
 }  // namespace
 
 hipError_t launch_quantize_mx(const QuantizeMxArgs& p, int x_type, hipStream_t s) {
-  const int64_t per = ((int64_t)p.K + 512 * UNROLL - 1) / (512 * UNROLL);
-  return launch_in_slices((p.M * per + 3) / 4, 256, [&](int64_t first, unsigned n) {
-    if (x_type == F32) hipLaunchKernelGGL((quantize_mx_kernel<F32>), dim3(n), dim3(256), 0, s, p, first, (int)per);
-    else if (x_type == F16) hipLaunchKernelGGL((quantize_mx_kernel<F16>), dim3(n), dim3(256), 0, s, p, first, (int)per);
-    else hipLaunchKernelGGL((quantize_mx_kernel<BF16>), dim3(n), dim3(256), 0, s, p, first, (int)per);
-  });
+  switch (x_type) {
+    case F32: return launch_type<F32>(p, s);
+    case F16: return launch_type<F16>(p, s);
+    case BF16: return launch_type<BF16>(p, s);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace tgemm

@@ -19,7 +19,7 @@ hipError_t launch_dispatch_rows(const RowArgs&, int type, hipStream_t);
 hipError_t launch_combine_rows(const RowArgs&, int type, hipStream_t);
 hipError_t launch_combine_rows_grad(const RowGradArgs&, int type, hipStream_t);
 hipError_t launch_quantize_mx(const QuantizeMxArgs&, int x_type, hipStream_t);
-hipError_t launch_stream_mx(const GemmParams&, const GroupArgs&, int c_type, int rows, int waves, hipStream_t);
+hipError_t launch_stream_mx(const GemmParams&, const GroupArgs&, int c_type, int rows, int columns, hipStream_t);
 // grouped_mfma.hpp's tiles (its GroupedTile numbers)
 hipError_t launch_grouped_mx_f16(const GemmParams&, const GroupArgs&, int tile, int cus, hipStream_t);
 hipError_t launch_grouped_mx_bf16(const GemmParams&, const GroupArgs&, int tile, int cus, hipStream_t);
@@ -197,7 +197,7 @@ int64_t step(int64_t ld, int64_t rows, int64_t least) { return rows > 1 ? ld : l
 bool stream_fits(const MxArgs& a) {
   const int64_t most = kMaxRowBytes;
   return step(a.lda, a.M, a.K) <= 2 * most && step(a.ldb, a.N, a.K) <= 2 * most && step(a.ldsa, a.M, 0) <= most &&
-         step(a.ldsb, a.N, 0) <= most && countable(a, 16, 32);
+         step(a.ldsb, a.N, 0) <= most && countable(a, 64, 32);
 }
 
 // The tiled kernels copy 16-byte chunks of the operands and their scales and store runs of C.
@@ -219,11 +219,34 @@ int64_t expected_tiles(const MxArgs& a, int64_t bm, int64_t bn) {
   return rows * ((a.N + bn - 1) / bn);
 }
 
+// Rows of a group that has any, on average.
+int64_t average_rows(const MxArgs& a) { return (a.M + live_groups(a) - 1) / live_groups(a); }
+
+// The kernel of a call (times: one MI355X, constant operands, 256 compute units).
 gemm_grouped_kernel_t pick(const MxArgs& a, int cus) {
-  const int64_t rows = (a.M + live_groups(a) - 1) / live_groups(a);
-  if (!tiles_fit(a) || (stream_fits(a) && rows <= 32)) return GEMM_GROUPED_STREAM;
-  if (2 * expected_tiles(a, 256, 256) >= cus) return GEMM_GROUPED_MFMA_256;
-  if (16 * expected_tiles(a, 128, 128) >= 9 * cus) return GEMM_GROUPED_MFMA_128;
+  const int64_t rows = average_rows(a), small = expected_tiles(a, 64, 64);
+  if (!tiles_fit(a)) return GEMM_GROUPED_STREAM;
+  if (stream_fits(a)) {
+    // Streaming needs no barrier and starts at once, but reads half lines, and the rows once for every 16 or
+    // 32 columns: it pays where 64 x 64 tiles are few.  One group: 1 x 28672 x 8192 (448 tiles) 26 us
+    // against 28, 16 x 28672 x 8192 35 against 31, 16 x 8192 x 4096 (128) 7.0 against 10.4, 48 rows 11.3
+    // against 10.4.  Many: 64 rows over 8 groups of 1024 x 1024 (80) 3.8 against 5.2, 32 over 64 of 1024 x 2048
+    // (272) 10.6 against 9.5, 64 over 32 of 2048 x 2048 (544) 18 against 14.  Very few: 64 x 4096 x 8192 (64)
+    // 14 against 20, 192 x 2048 x 2048 (96) 7.3 against 6.3.
+    const bool one = a.groups == 1;
+    if ((one && a.M <= 8) || (rows <= 32 && 4 * small <= (one ? 6 : 3) * cus) || (rows <= 128 && 4 * small <= cus))
+      return GEMM_GROUPED_STREAM;
+  }
+  // Large tiles, mixed with small ones, from 5/8 of a round on, with uneven groups from 3/8 on if they hold
+  // large tiles at all (1536 x 8192 x 1024, 192 of them, 13.5 us against 15.1 on 128 x 128 ones, 2048 x 4096 x
+  // 4096, 128, 33 against 23; 2048 rows over 8 groups of 4096 x 4096, 128, 30 against 36, but 4096 over 32 of
+  // 2048 x 2048, 128, 31 against 24).
+  const int64_t large = a.M * ((a.N + 255) / 256);  // in rows of 256
+  if (a.groups == 1 ? 8 * large >= 5 * 256 * cus : rows >= 160 && 8 * large >= 3 * 256 * cus) return GEMM_GROUPED_MFMA_256;
+  // 128 x 128 from most of a round on (1024 x 4096 x 4096, 256 of them, 17.2 us against 20.8 on 64 x 64 ones,
+  // 1024 x 2048 x 2048, 128, 10.4 against 8.2), and with groups that fill them (64 rows a group 24.5 against
+  // 19.2, 96 rows 24.2 against 24.3, 128 rows 24.1 against 26.3: 32 groups of 2048 x 2048).
+  if (8 * expected_tiles(a, 128, 128) >= 7 * cus && (a.groups == 1 || rows >= 96)) return GEMM_GROUPED_MFMA_128;
   return GEMM_GROUPED_MFMA_64;
 }
 
@@ -260,16 +283,21 @@ gemm_status_t run(gemm_handle_t h, gemm_grouped_kernel_t kernel, void* stream, c
   const hipStream_t s = static_cast<hipStream_t>(stream);
   tgemm::DeviceGuard g(h->device);
   if (kernel == GEMM_GROUPED_STREAM) {
-    // rows of a workgroup: what a group has on average, less while there are compute units to spare
-    const int64_t avg = (a.M + live_groups(a) - 1) / live_groups(a);
-    int rows = avg <= (a.groups == 1 ? 16 : 10) ? 16 : avg <= (a.groups == 1 ? 32 : 24) ? 32 : 64;
-    while (rows > 16 && 4 * expected_tiles(a, rows, 32) <= 3 * h->cu_count) rows /= 2;
-    if (!countable(a, rows, 32)) rows = 64;
+    // A workgroup has as few rows as leave the compute units at most 1.6 workgroups each (24 x 8192 x 4096 with
+    // 16 rows, 512 of them, 9.9 us, with 32 8.3; 37 x 4101 x 4128, 387, 6.9 and 8.9; 48 x 8192 x 4096 with 32, 512,
+    // 14.3, with 64 11.3), and half the columns where that is not one each (16 x 4096 x 8192 7.8 us against 9.6,
+    // 16 x 8192 x 4096, two each, 7.4 against 7.1) or rows weigh little (1 x 28672 x 8192 26 against 29).
+    int rows = 16;
+    while (rows < 64 && rows < 2 * average_rows(a) && 10 * expected_tiles(a, rows, 32) > 16 * h->cu_count) rows *= 2;
+    while (rows < 64 && !countable(a, rows, 32)) rows *= 2;
+    const bool narrow = rows == 16 && countable(a, 16, 16) &&
+                        ((a.groups == 1 && a.M <= 8) || expected_tiles(a, 16, 16) <= h->cu_count);
     p.ldsa = step(a.ldsa, a.M, 0);
     p.ldsb = step(a.ldsb, a.N, 0);
-    return status(tgemm::launch_stream_mx(p, ga, a.ct, rows, 8, s));
+    return status(tgemm::launch_stream_mx(p, ga, a.ct, rows, narrow ? 16 : 32, s));
   }
-  const int tile = kernel == GEMM_GROUPED_MFMA_64 ? 1 : kernel == GEMM_GROUPED_MFMA_128 ? 2 : 3;
+  const bool deep = a.K >= 4096 && expected_tiles(a, 64, 64) <= 2 * h->cu_count;  // three stages (GroupedMxCfg)
+  const int tile = kernel == GEMM_GROUPED_MFMA_64 ? (deep ? 4 : 1) : kernel == GEMM_GROUPED_MFMA_128 ? 2 : 3;
   return status(a.ct == GEMM_F32   ? tgemm::launch_grouped_mx_f32(p, ga, tile, h->cu_count, s)
                 : a.ct == GEMM_F16 ? tgemm::launch_grouped_mx_f16(p, ga, tile, h->cu_count, s)
                                    : tgemm::launch_grouped_mx_bf16(p, ga, tile, h->cu_count, s));
