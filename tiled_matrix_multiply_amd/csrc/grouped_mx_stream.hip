@@ -63,6 +63,24 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(GemmParams p, GroupA
     osb[f] = r * (uint32_t)p.ldsb;
   }
 
+  // What the thread finishes at the end: items of four columns, and their bias, which would otherwise come in
+  // after the sums, with nothing left to hide its way from memory (32 rows over 64 groups of 1024 x 2048 with
+  // bias and GELU FIGB).
+  constexpr int ITEMS = NF * MF * 64, MINE = (ITEMS + 64 * NW - 1) / (64 * NW);
+  auto item = [&](int i, int& m, int& n) {
+    m = m0 + 16 * ((i >> 6) % MF) + (i & 15);
+    n = n0 + 16 * ((i >> 6) / MF) + 4 * ((i & 63) >> 4);
+    return (ITEMS % (64 * NW) == 0 || i < ITEMS) && m < p.M && n < p.N;
+  };
+  float bj[MINE][4];
+#pragma unroll
+  for (int t = 0; t < MINE; ++t) {
+    int m, n;
+    const bool live = (p.epi & EPI_BIAS) && item(threadIdx.x + 64 * NW * t, m, n);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bj[t][e] = live ? p.bias[min(n + e, p.N - 1)] : 0.0f;  // past the edge the last once more
+  }
+
   struct Unit {
     x_u32x4 b[NF][U], a[MF][U];
     uint32_t sb[NF][U], sa[MF][U];
@@ -127,27 +145,17 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(GemmParams p, GroupA
       for (int f = 0; f < MF; ++f) acc[j][f] = mma_mx(b[j], a[f], acc[j][f], sb[j], sa[f]);
   };
 
-  // Whole units over the waves in turn, two in flight each; the steps after the last whole unit go to
-  // one wave each, before its units.
+  // Whole units over the waves in turn; the steps after the last whole unit go to one wave each, before its
+  // units.  A wave has one unit in flight at a time: a second one ahead would cost it the registers of two
+  // more waves beside it, which hide as much (with one unit ahead, 32 rows over 64 groups of 1024 x 2048 10.2 us
+  // against 8.2, 256 over 32 of 2048 x 2048 21.3 against 16.2, 1 x 16384 x 16384 37.5 against 31.5, 16 x 28672 x 8192
+  // 35.7 against 37.2).
   const int steps = (int)(((int64_t)p.K + 63) / 64), units = p.K / (64 * U), first = units * U;
   for (int s = first + wave; s < steps; s += NW) rest_step(s);
-  if (wave < units) {
-    Unit x, y;
-    int b = wave;
+  for (int b = wave; b < units; b += NW) {
+    Unit x;
     load(b, x);
-    for (; b + 2 * NW < units; b += 2 * NW) {
-      load(b + NW, y);
-      mul(x);
-      load(b + 2 * NW, x);
-      mul(y);
-    }
-    if (b + NW < units) {
-      load(b + NW, y);
-      mul(x);
-      mul(y);
-    } else {
-      mul(x);
-    }
+    mul(x);
   }
 
 #pragma unroll
@@ -159,24 +167,23 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(GemmParams p, GroupA
   // A lane of fragment (j, f) holds row 16 f + l16 and, in register r, column 16 j + 4 q + r.
   auto finish = [&](auto ct) {
     constexpr int CT = decltype(ct)::value;
-    for (int i = threadIdx.x; i < NF * MF * 64; i += 64 * NW) {
-      const int l = i & 63, jf = i >> 6;
-      const int m = m0 + 16 * (jf % MF) + (l & 15), n = n0 + 16 * (jf / MF) + 4 * (l >> 4);
-      if (m >= p.M || n >= p.N) continue;
-      float bj[4], cin[4];  // all reads together, past the edge the last column once more
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int col = min(n + e, p.N - 1);
-        bj[e] = (p.epi & EPI_BIAS) ? p.bias[col] : 0.0f;
-        cin[e] = p.beta != 0.0f ? load_as_float<CT>(p.C, (int64_t)m * p.ldc + col) : 0.0f;
+    for (int t = 0; t < MINE; ++t) {
+      const int i = threadIdx.x + 64 * NW * t;
+      int m, n;
+      if (!item(i, m, n)) continue;
+      float cin[4] = {};
+      if (p.beta != 0.0f) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) cin[e] = load_as_float<CT>(p.C, (int64_t)m * p.ldc + min(n + e, p.N - 1));
       }
       x_f32x4 v = x_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int w = 0; w < NW; ++w) v += part[w][jf][l];
+      for (int w = 0; w < NW; ++w) v += part[w][i >> 6][i & 63];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (n + e < p.N)
-          store_from_float<CT>(p.C, (int64_t)m * p.ldc + n + e, epilogue_value<CT>(v[e], p.alpha, p.beta, cin[e], bj[e], p.epi));
+          store_from_float<CT>(p.C, (int64_t)m * p.ldc + n + e, epilogue_value<CT>(v[e], p.alpha, p.beta, cin[e], bj[t][e], p.epi));
     }
   };
   if (c_type == F32) finish(std::integral_constant<int, F32>{});
@@ -199,11 +206,15 @@ hipError_t launch_cfg(GemmParams p, GroupArgs ga, int c_type, hipStream_t s) {
 
 // rows: 16, 32 or 64 rows of C per workgroup; columns: 16 (with 16 rows only) or 32.
 hipError_t launch_stream_mx(const GemmParams& p, const GroupArgs& ga, int c_type, int rows, int columns, hipStream_t s) {
-  if (columns == 16) return rows == 16 ? launch_cfg<1, 1, 4>(p, ga, c_type, s) : hipErrorInvalidValue;
+  if (columns == 16) {
+    if (rows != 16) return hipErrorInvalidValue;
+    // longer units where every wave has one (1 x 28672 x 8192 23.7 us against 26.9, 1 x 57344 x 2880 17.6 against 16.2)
+    return p.K >= 6 * 64 * 8 ? launch_cfg<1, 1, 8>(p, ga, c_type, s) : launch_cfg<1, 1, 4>(p, ga, c_type, s);
+  }
   switch (rows) {
     case 16: return launch_cfg<2, 1, 4>(p, ga, c_type, s);
-    case 32: return launch_cfg<2, 2, 2>(p, ga, c_type, s);
-    case 64: return launch_cfg<2, 4, 2>(p, ga, c_type, s);
+    case 32: return launch_cfg<2, 2, 4>(p, ga, c_type, s);
+    case 64: return launch_cfg<2, 4, 4>(p, ga, c_type, s);
     default: return hipErrorInvalidValue;
   }
 }

@@ -228,13 +228,15 @@ gemm_grouped_kernel_t pick(const MxArgs& a, int cus) {
   if (!tiles_fit(a)) return GEMM_GROUPED_STREAM;
   if (stream_fits(a)) {
     // Streaming needs no barrier and starts at once, but reads half lines, and the rows once for every 16 or
-    // 32 columns: it pays where 64 x 64 tiles are few.  One group: 1 x 28672 x 8192 (448 tiles) 26 us
-    // against 28, 16 x 28672 x 8192 35 against 31, 16 x 8192 x 4096 (128) 7.0 against 10.4, 48 rows 11.3
-    // against 10.4.  Many: 64 rows over 8 groups of 1024 x 1024 (80) 3.8 against 5.2, 32 over 64 of 1024 x 2048
-    // (272) 10.6 against 9.5, 64 over 32 of 2048 x 2048 (544) 18 against 14.  Very few: 64 x 4096 x 8192 (64)
-    // 14 against 20, 192 x 2048 x 2048 (96) 7.3 against 6.3.
+    // 32 columns: it pays where 64 x 64 tiles are few.  One group: 1 x 28672 x 8192 (448 tiles) 24 us against
+    // 28, 16 x 28672 x 8192 37 against 31, 16 x 8192 x 4096 (128) 6.5 against 10.4, 48 rows 10.2 against 10.4.
+    // Many: 64 rows over 8 groups of 1024 x 1024 (80) 3.7 against 5.2, 32 over 64 of 1024 x 2048 (272) 8.2 against
+    // 9.5, 64 over 32 of 2048 x 2048 (544, 2 rows a group) 13.5 against 14.2, 256 rows 16.2 against 14.2, 128 over
+    // 16 of 4096 x 4096 (640) 38 against 30.  Very few: 64 x 4096 x 8192 (64) 14 against 20, 192 x 2048 x 2048 (96)
+    // 7.3 against 6.3.
     const bool one = a.groups == 1;
-    if ((one && a.M <= 8) || (rows <= 32 && 4 * small <= (one ? 6 : 3) * cus) || (rows <= 128 && 4 * small <= cus))
+    const int64_t most = (one ? 6 : rows <= 4 ? 10 : 5) * cus;
+    if ((one && a.M <= 8) || (rows <= 32 && 4 * small <= most) || (rows <= 128 && 4 * small <= cus))
       return GEMM_GROUPED_STREAM;
   }
   // Large tiles, mixed with small ones, from 5/8 of a round on, with uneven groups from 3/8 on if they hold
@@ -283,10 +285,11 @@ gemm_status_t run(gemm_handle_t h, gemm_grouped_kernel_t kernel, void* stream, c
   const hipStream_t s = static_cast<hipStream_t>(stream);
   tgemm::DeviceGuard g(h->device);
   if (kernel == GEMM_GROUPED_STREAM) {
-    // A workgroup has as few rows as leave the compute units at most 1.6 workgroups each (24 x 8192 x 4096 with
-    // 16 rows, 512 of them, 9.9 us, with 32 8.3; 37 x 4101 x 4128, 387, 6.9 and 8.9; 48 x 8192 x 4096 with 32, 512,
-    // 14.3, with 64 11.3), and half the columns where that is not one each (16 x 4096 x 8192 7.8 us against 9.6,
-    // 16 x 8192 x 4096, two each, 7.4 against 7.1) or rows weigh little (1 x 28672 x 8192 26 against 29).
+    // A workgroup has as few rows as leave the compute units at most 1.6 workgroups each (48 x 8192 x 4096 with
+    // 16 rows, 768 of them, 13.0 us, with 32 12.4, with 64 10.2; 37 x 4104 x 4128, 387, 6.6, 7.2 and 7.4), and half
+    // the columns where that is not one each (1 x 4096 x 4096 4.0 against 5.2, 16 x 8192 x 4096, two each, 7.4 against
+    // 6.5) or rows weigh little: twice as many workgroups even out the last round (1 x 20480 x 7168 14.3 against
+    // 15.7, 1 x 16384 x 7168, two each exactly, 12.1 against 11.4).
     int rows = 16;
     while (rows < 64 && rows < 2 * average_rows(a) && 10 * expected_tiles(a, rows, 32) > 16 * h->cu_count) rows *= 2;
     while (rows < 64 && !countable(a, rows, 32)) rows *= 2;
