@@ -189,15 +189,16 @@ struct Layout {
 
 // The n <= V logits of a lane from expert e on, -infinity after them.
 template <int V>
-__device__ __forceinline__ void load_logits(const RouteArgs& p, int64_t t, int e, int n, float (&x)[V]) {
-  const int64_t at = t * p.ldx + e;
+__device__ __forceinline__ void load_logits(const void* logits, int64_t ldx, int type, int64_t t, int e, int n,
+                                            float (&x)[V]) {
+  const int64_t at = t * ldx + e;
   if (n == V && V > 1) {  // all loads together, of any alignment
-    if (p.x_type == F32) {
-      __builtin_memcpy(x, reinterpret_cast<const float*>(p.x) + at, 4 * V);
+    if (type == F32) {
+      __builtin_memcpy(x, reinterpret_cast<const float*>(logits) + at, 4 * V);
     } else {
       uint32_t w[(V + 1) / 2] = {};
-      __builtin_memcpy(w, reinterpret_cast<const uint16_t*>(p.x) + at, 2 * V);
-      if (p.x_type == F16) {
+      __builtin_memcpy(w, reinterpret_cast<const uint16_t*>(logits) + at, 2 * V);
+      if (type == F16) {
 #pragma unroll
         for (int i = 0; i < V; ++i) x[i] = f16_bits_to_float((w[i / 2] >> (16 * (i & 1))) & 0xffffu);
       } else {
@@ -207,7 +208,27 @@ __device__ __forceinline__ void load_logits(const RouteArgs& p, int64_t t, int e
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = i < n ? load_logit(p.x, at + i, p.x_type) : kNone;
+    for (int i = 0; i < V; ++i) x[i] = i < n ? load_logit(logits, at + i, type) : kNone;
+  }
+}
+
+// n <= V results of a lane from element `at` on, rounded once; all together where there are V, of any
+// alignment.
+template <int CT, int V>
+__device__ __forceinline__ void store_run(void* to, int64_t at, int n, const float (&v)[V]) {
+  if (n == V && V > 1) {
+    if constexpr (CT == F32) {
+      __builtin_memcpy(reinterpret_cast<float*>(to) + at, v, 4 * V);
+    } else {
+      uint32_t w[(V + 1) / 2] = {};
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i / 2] |= (CT == F16 ? float_to_f16_bits(v[i]) : float_to_bf16_bits(v[i])) << (16 * (i & 1));
+      __builtin_memcpy(reinterpret_cast<uint16_t*>(to) + at, w, 2 * V);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) store_from_float<CT>(to, at + i, v[i]);
   }
 }
 
@@ -534,6 +555,15 @@ __device__ __forceinline__ float exp_near(float v) {
   return fabsf(v) < 80.0f ? fmaf(e, rest * 0.693147181f, e) : e;  // (past that e or the rest may be no number)
 }
 
+// A chosen score relative to the largest chosen logit, so that their sum is at least 1/2: exp(x - top) for
+// softmax; for sigmoid exp(x - m) / (1 + exp(x)) with m = min(top, 0), the score times exp(-m).
+__device__ __forceinline__ float score_near(int sigmoid, float x, float top) {
+  if (!sigmoid) return exp_near(x - top);
+  // x > 0: then m = 0 and the score is 1 / (1 + exp(-x))
+  const float e = exp_near(x > 0.0f ? -x : x);
+  return (x > 0.0f ? 1.0f : exp_near(x - fminf(top, 0.0f))) * __builtin_amdgcn_rcpf(1.0f + e);
+}
+
 // Weight of the lane's chosen expert among the token's: p.top lanes hold one each.
 template <int L, int V>
 __device__ __forceinline__ float weight_of(const RouteArgs& p, int chosen, float cx, float x_max, float sum) {
@@ -542,18 +572,8 @@ __device__ __forceinline__ float weight_of(const RouteArgs& p, int chosen, float
     const float s = p.score ? __builtin_amdgcn_rcpf(1.0f + exp_near(-cx)) : exp_near(cx - x_max) / sum;
     return there ? p.scale * s : 0.0f;
   }
-  // Relative to the largest chosen logit, so that the sum is at least 1/2: exp(x - m) for softmax; for
-  // sigmoid exp(x - m) / (1 + exp(x)) with m = min(largest, 0), the scores times exp(-m).
   const float top = max_across<L>(there ? (cx != cx ? __builtin_inff() : cx) : kNone);
-  const float m = p.score ? fminf(top, 0.0f) : top;
-  float s = 0.0f;
-  if (p.score) {
-    // x > 0: then m = 0 and the score is 1 / (1 + exp(-x))
-    const float e = exp_near(cx > 0.0f ? -cx : cx);
-    s = (cx > 0.0f ? 1.0f : exp_near(cx - m)) * __builtin_amdgcn_rcpf(1.0f + e);
-  } else {
-    s = exp_near(cx - m);
-  }
+  float s = score_near(p.score, cx, top);
   if (!there) s = 0.0f;
   const float all = sum_across<L>(s);
   return there ? p.scale * (s / all) : 0.0f;
@@ -566,7 +586,7 @@ __device__ __forceinline__ void choose_again(const RouteArgs& p, int run_lanes, 
                                              float& cx) {
   const Layout lay(p, run_lanes);
   float x[VV];
-  load_logits<VV>(p, t, lay.expert<VV>(lane), lay.count<VV>(lane), x);
+  load_logits<VV>(p.x, p.ldx, p.x_type, t, lay.expert<VV>(lane), lay.count<VV>(lane), x);
   float x_max = 0.0f;
   double sum = 1.0;
   if (!p.score && (p.bias || (p.groups > 1 && p.group_top == 2))) {
@@ -616,7 +636,7 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs p, int TB) {
     const bool live = local < here;
     const int64_t t = t0 + (live ? local : here - 1);
     float x[V];
-    load_logits<V>(p, t, e0, n, x);
+    load_logits<V>(p.x, p.ldx, p.x_type, t, e0, n, x);
     const bool scored = p.bias || (p.groups > 1 && p.group_top == 2);
     float x_max = 0.0f, sum = 1.0f;
     if (scored || (!p.score && !p.renorm)) {
@@ -801,10 +821,17 @@ __global__ __launch_bounds__(256) void route_place_kernel(RouteArgs p, int TB, i
 //   dx_e = s_e (g_e - sum_j g_j s_j) = s_e (g_e U + sum_j s_j (g_e - g_j)),   U = the sum of the others' s
 // (g_e = 0 for what was not chosen).  Written as differences none of them cancels where one weight is
 // near 1.
+// A token's row of results lies in LDS between what every expert gets and what the chosen get; only the
+// wave that owns it touches it, so its writes and reads keep their order without a barrier.
+__device__ __forceinline__ void row_written() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 template <int L, int V>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
   constexpr int TW = 64 / L;
-  __shared__ float row[4 * TW][L * V];
+  __shared__ __attribute__((aligned(16))) float row[4 * TW][L * V];
   const int tid = threadIdx.x, lane = tid & 63, sub = lane & (L - 1);
   const int64_t t = (int64_t)blockIdx.x * (4 * TW) + tid / L;
   const bool live = t < p.T;
@@ -815,72 +842,77 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
   float g = 0.0f, cx = kNone;
   if (sub < p.top) {
     e = p.expert[tt * p.top + sub];
-    if (e < 0 || e >= p.E) e = -1;
-    if (e >= 0) {
-      g = p.scale * p.dw[tt * p.top + sub];
+    g = p.scale * p.dw[tt * p.top + sub];
+    if (e < 0 || e >= p.E) {
+      e = -1;
+      g = 0.0f;
+    } else {
       cx = load_logit(p.x, tt * p.ldx + e, p.x_type);
     }
   }
+  const int e0 = sub * V, n = min(max(p.E - e0, 0), V);
   const bool full = !p.score && !p.renorm;  // every logit has a gradient
-  float s_all[V], sum = 1.0f, x_max = 0.0f, others = 0.0f;
+  float v[V], sum = 1.0f, x_max = 0.0f, others = 0.0f;
   if (full) {
-    float x[V];
+    load_logits<V>(p.x, p.ldx, p.x_type, tt, e0, n, v);
+    x_max = largest<L, V>(v);
+    // the scores; then once more without the chosen's
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int k = sub * V + i;
-      x[i] = k < p.E ? load_logit(p.x, tt * p.ldx + k, p.x_type) : kNone;
-    }
-    x_max = largest<L, V>(x);
-    sum = softmax_sum<L, V, float>(x, x_max);
-    uint32_t taken = 0;  // which of the lane's experts were chosen
-    for (int j = 0; j < p.top; ++j) {
-      const int k = __shfl(e, (lane & ~(L - 1)) + j);
-      if (k >= 0 && k / V == sub) taken |= 1u << (k % V);
-    }
+    for (int i = 0; i < V; ++i) v[i] = v[i] == kNone ? 0.0f : exp_near(v[i] - x_max);
+    sum = sum_across<L>(lane_sum<V>(v));
+    const float r = 1.0f / sum;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      s_all[i] = x[i] == kNone ? 0.0f : expf(x[i] - x_max) / sum;
-      if (!((taken >> i) & 1)) others += s_all[i];
-    }
-    others = sum_across<L>(others);
+    for (int i = 0; i < V; ++i) mine[e0 + i] = v[i] * r;
+    row_written();
+    if (e >= 0) mine[e] = 0.0f;
+    row_written();
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = mine[e0 + i];
+    others = sum_across<L>(lane_sum<V>(v));
   }
   float s;  // of the chosen, relative to a common factor with renorm
   if (p.renorm) {
     const float top = max_across<L>(e >= 0 ? (cx != cx ? __builtin_inff() : cx) : kNone);
-    const float m = p.score ? fminf(top, 0.0f) : top;
-    s = !p.score ? expf(cx - m) : cx > 0.0f ? 1.0f / (1.0f + expf(-cx)) : expf(cx - m) / (1.0f + expf(cx));
+    s = score_near(p.score, cx, top);
     if (e < 0) s = 0.0f;
     s = s / sum_across<L>(s);
   } else {
-    s = p.score ? 1.0f / (1.0f + expf(-cx)) : expf(cx - x_max) / sum;
+    s = p.score ? __builtin_amdgcn_rcpf(1.0f + exp_near(-cx)) : exp_near(cx - x_max) / sum;
   }
   if (e < 0) s = 0.0f;
+  // sums over the chosen: of s (g_e - g) and of s g
   float d = 0.0f, dot = 0.0f;
-  for (int j = 0; j < p.top; ++j) {
-    const int from = (lane & ~(L - 1)) + j;
-    const float sj = __shfl(s, from), gj = __shfl(g, from);
-    const bool there = __shfl(e, from) >= 0;
-    if (there) {
-      d += sj * (g - gj);
-      dot += sj * gj;
+  if constexpr (L == 64) {
+    for (int j = 0; j < p.top; ++j) {
+      const float sj = lane_value(s, j);
+      d = fmaf(sj, g - lane_value(g, j), d);
     }
+  } else {
+#define TGEMM_TURN(r) d = fmaf(dpp<0x120 + r>(s), g - dpp<0x120 + r>(g), d)
+    TGEMM_TURN(1); TGEMM_TURN(2); TGEMM_TURN(3); TGEMM_TURN(4); TGEMM_TURN(5);
+    TGEMM_TURN(6); TGEMM_TURN(7); TGEMM_TURN(8); TGEMM_TURN(9); TGEMM_TURN(10);
+    TGEMM_TURN(11); TGEMM_TURN(12); TGEMM_TURN(13); TGEMM_TURN(14); TGEMM_TURN(15);
+#undef TGEMM_TURN
   }
-  if (full) d = s * fmaf(g, others, d);
-  else if (p.renorm) d = s * d;
-  else d = s * g;
-  if (p.score) d *= 1.0f / (1.0f + expf(cx));
+  if (full) {
+    dot = sum_across<L>(s * g);
+    d = s * fmaf(g, others, d);
+  } else {
+    d = p.renorm ? s * d : s * g;
+  }
+  if (p.score) d *= __builtin_amdgcn_rcpf(1.0f + exp_near(cx));
 #pragma unroll
-  for (int i = 0; i < V; ++i) mine[sub * V + i] = full ? -s_all[i] * dot : 0.0f;
-  __syncthreads();
+  for (int i = 0; i < V; ++i) mine[e0 + i] = full ? -v[i] * dot : 0.0f;
+  row_written();
   if (e >= 0) mine[e] = cx == kNone ? 0.0f : d;
-  __syncthreads();
+  row_written();
   if (!live) return;
-  for (int k = sub; k < p.E; k += L) {
-    const int64_t at = t * p.ldd + k;
-    if (p.x_type == F32) store_from_float<F32>(p.dx, at, mine[k]);
-    else if (p.x_type == F16) store_from_float<F16>(p.dx, at, mine[k]);
-    else store_from_float<BF16>(p.dx, at, mine[k]);
-  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = mine[e0 + i];
+  const int64_t at = t * p.ldd + e0;
+  if (p.x_type == F32) store_run<F32, V>(p.dx, at, n, v);
+  else if (p.x_type == F16) store_run<F16, V>(p.dx, at, n, v);
+  else store_run<BF16, V>(p.dx, at, n, v);
 }
 
 template <int L, int V, int MOST>
@@ -949,8 +981,11 @@ static hipError_t grad_launch(const RouteGradArgs& p, hipStream_t s) {
 }
 
 hipError_t launch_route_grad(const RouteGradArgs& p, hipStream_t s) {
-  if (p.E <= 32 && p.top <= 16) return grad_launch<16, 2>(p, s);
-  if (p.E <= 256 && p.top <= 16) return grad_launch<16, 16>(p, s);
+  if (p.top <= 16) {  // 16 lanes hold them
+    if (p.E <= 64) return grad_launch<16, 4>(p, s);
+    if (p.E <= 128) return grad_launch<16, 8>(p, s);
+    if (p.E <= 256) return grad_launch<16, 16>(p, s);
+  }
   if (p.E <= 256) return grad_launch<64, 4>(p, s);
   return grad_launch<64, 16>(p, s);
 }
