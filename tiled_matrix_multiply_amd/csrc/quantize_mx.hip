@@ -98,11 +98,11 @@ hipError_t launch_unroll(const QuantizeMxArgs& p, hipStream_t s) {
   });
 }
 
-// Four groups a wave keep four loads in flight; a small matrix spreads over more waves instead (1 x 8192
-// 4.0 us against 4.7, 37 x 4128 2.9 against 3.8).
+// Two groups of 512 elements a wave, one where the row has no second (bf16, 16384 x 4096: 33.8 us with one,
+// 29.5 with two, 33.3 with four; 65536 x 512: 15.7, 17.1, 24.6; 1 x 8192: 2.6, 2.5, 2.7).
 template <int XT>
 hipError_t launch_type(const QuantizeMxArgs& p, hipStream_t s) {
-  return (int64_t)p.M * p.K <= 512 * 4096 ? launch_unroll<XT, 1>(p, s) : launch_unroll<XT, 4>(p, s);
+  return p.K <= 512 ? launch_unroll<XT, 1>(p, s) : launch_unroll<XT, 2>(p, s);
 }
 
 }  // namespace

@@ -2,7 +2,9 @@
 //
 // Everything goes by tokens: the places of a token's pairs are a few neighbouring numbers, a token's row
 // is read (or written) once, and the experts' rows are whole rows, so that each 16-byte access of a wave
-// lies in one run of 1 KB whatever the order.  What bounds it is the bytes.
+// lies in one run of 1 KB whatever the order.  What bounds it is the bytes: 8190 tokens of 8 x 2048 in bf16
+// dispatched in 58.5 us (5.16 TB/s), combined in 60.4 (5.00), the gradient 117.4 (4.86), where a copy of
+// 4 GiB runs at 4.63.
 #include <type_traits>
 
 #include "experts.hpp"
@@ -65,78 +67,104 @@ __device__ __forceinline__ m_u32x4 pack(const float* f) {
   return v;
 }
 
-// The work of dispatch and combine comes in pieces, 64 lanes x UNROLL chunks of one token's row, one to a
-// wave.
-constexpr int UNROLL = 4;
-inline int64_t pieces(int64_t K, int es) { return (K * es + 64 * 16 * UNROLL - 1) / (64 * 16 * UNROLL); }
+// The work of dispatch and combine comes in pieces of 64 chunks of one token's row, one to a wave.  (Four
+// chunks a lane, the loads together, were slower everywhere: fewer waves have more to wait for.  4096 tokens
+// to 2 places of 4096: dispatch 16.1 us with one, 16.0 with two, 16.4 with four; combine 19.4, 21.1, 23.6;
+// 512 tokens to 8: dispatch 7.5, 7.6, 8.7, combine 7.6, 9.1, 14.7.)
+inline int64_t pieces(int64_t K, int es) { return (K * es + 64 * 16 - 1) / (64 * 16); }
+
+// A wave's token and chunk.
+struct Piece {
+  int64_t t, c;
+  __device__ __forceinline__ Piece(int64_t first, int per) {
+    const int64_t item = (first + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    t = item / per;
+    c = (item - t * per) * 64 + (threadIdx.x & 63);
+  }
+};
 
 template <int ES>
 __global__ __launch_bounds__(256) void dispatch_kernel(RowArgs p, int64_t first, int per) {
-  const int lane = threadIdx.x & 63;
-  const int64_t item = (first + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = item / per;
-  if (t >= p.T) return;
-  const int64_t c0 = (item - t * per) * (64 * UNROLL) + lane, chunks = ((int64_t)p.K * ES + 15) / 16;
-  const uint8_t* const src = reinterpret_cast<const uint8_t*>(p.X) + t * p.ldx * ES;
-  m_u32x4 v[UNROLL];
-#pragma unroll
-  for (int u = 0; u < UNROLL; ++u)
-    if (c0 + 64 * u < chunks) v[u] = load_chunk<ES>(src, c0 + 64 * u, p.K);
+  const Piece at(first, per);
+  if (at.t >= p.T || at.c * (16 / ES) >= p.K) return;
+  const m_u32x4 v = load_chunk<ES>(reinterpret_cast<const uint8_t*>(p.X) + at.t * p.ldx * ES, at.c, p.K);
   for (int j = 0; j < p.top; ++j) {
-    const int at = p.place[t * p.top + j];
-    if (at < 0 || at >= p.R) continue;
-    uint8_t* const dst = reinterpret_cast<uint8_t*>(p.Y) + at * p.ldy * ES;
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
-      if (c0 + 64 * u < chunks) store_chunk<ES>(dst, c0 + 64 * u, p.K, v[u]);
+    const int row = p.place[at.t * p.top + j];
+    if (row < 0 || row >= p.R) continue;
+    store_chunk<ES>(reinterpret_cast<uint8_t*>(p.Y) + row * p.ldy * ES, at.c, p.K, v);
   }
 }
 
-template <int DT>
+// Places of a token's J pairs from j on, which of them are rows at all, and their weights.  (A row that is
+// none is read as row 0 and not used: loads outside branches go out together.)
+template <int J>
+struct Pairs {
+  int at[J];
+  bool ok[J];
+  float w[J];
+  __device__ __forceinline__ Pairs(const int32_t* place, const float* weight, int64_t first, int j, int top, int R) {
+#pragma unroll
+    for (int q = 0; q < J; ++q) {
+      const int64_t pair = first + min(j + q, top - 1);
+      const int row = place[pair];
+      ok[q] = j + q < top && row >= 0 && row < R;
+      at[q] = row >= 0 && row < R ? row : 0;
+      w[q] = weight ? weight[pair] : 1.0f;
+    }
+  }
+};
+
+template <int DT, int J>
 __global__ __launch_bounds__(256) void combine_kernel(RowArgs p, int64_t first, int per) {
   constexpr int ES = DTypeInfo<DT>::bytes, CE = 16 / ES;
-  const int lane = threadIdx.x & 63;
-  const int64_t item = (first + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = item / per;
-  if (t >= p.T) return;
-  const int64_t c0 = (item - t * per) * (64 * UNROLL) + lane, chunks = ((int64_t)p.K * ES + 15) / 16;
-  float sum[UNROLL][CE] = {};
-  for (int j = 0; j < p.top; ++j) {
-    const int at = p.place[t * p.top + j];
-    if (at < 0 || at >= p.R) continue;
-    const float w = p.weight ? p.weight[t * p.top + j] : 1.0f;
-    const uint8_t* const src = reinterpret_cast<const uint8_t*>(p.X) + at * p.ldx * ES;
-    m_u32x4 v[UNROLL];
+  const Piece at(first, per);
+  if (at.t >= p.T || at.c * CE >= p.K) return;
+  float sum[CE] = {};
+  for (int j = 0; j < p.top && p.R > 0; j += J) {
+    const Pairs<J> pairs(p.place, p.weight, at.t * p.top, j, p.top, p.R);
+    m_u32x4 v[J];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
-      if (c0 + 64 * u < chunks) v[u] = load_chunk<ES>(src, c0 + 64 * u, p.K);
+    for (int q = 0; q < J; ++q)
+      v[q] = load_chunk<ES>(reinterpret_cast<const uint8_t*>(p.X) + pairs.at[q] * p.ldx * ES, at.c, p.K);
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
-      if (c0 + 64 * u < chunks)
+    for (int q = 0; q < J; ++q) {
+      if (!pairs.ok[q]) continue;
 #pragma unroll
-        for (int e = 0; e < CE; ++e) sum[u][e] = fmaf(w, element<DT>(v[u], e), sum[u][e]);
-  }
-  uint8_t* const dst = reinterpret_cast<uint8_t*>(p.Y) + t * p.ldy * ES;
-#pragma unroll
-  for (int u = 0; u < UNROLL; ++u) {
-    if (c0 + 64 * u >= chunks) continue;
-    if (p.beta != 0.0f) {
-      const m_u32x4 c = load_chunk<ES>(dst, c0 + 64 * u, p.K);
-#pragma unroll
-      for (int e = 0; e < CE; ++e) sum[u][e] = fmaf(p.beta, element<DT>(c, e), sum[u][e]);
+      for (int e = 0; e < CE; ++e) sum[e] = fmaf(pairs.w[q], element<DT>(v[q], e), sum[e]);
     }
-    store_chunk<ES>(dst, c0 + 64 * u, p.K, pack<DT>(sum[u]));
   }
+  uint8_t* const dst = reinterpret_cast<uint8_t*>(p.Y) + at.t * p.ldy * ES;
+  if (p.beta != 0.0f) {
+    const m_u32x4 c = load_chunk<ES>(dst, at.c, p.K);
+#pragma unroll
+    for (int e = 0; e < CE; ++e) sum[e] = fmaf(p.beta, element<DT>(c, e), sum[e]);
+  }
+  store_chunk<ES>(dst, at.c, p.K, pack<DT>(sum));
+}
+
+// The sum over a wave, in every lane, in a fixed order.
+__device__ __forceinline__ float wave_sum(float v) {
+  auto turn = [](float x, auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xf, 0xf, false));
+  };
+  v += turn(v, std::integral_constant<int, 0x128>{});  // row_ror 8, 4, 2, 1
+  v += turn(v, std::integral_constant<int, 0x124>{});
+  v += turn(v, std::integral_constant<int, 0x122>{});
+  v += turn(v, std::integral_constant<int, 0x121>{});
+  auto of = [](float x, int l) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), l)); };
+  return (of(v, 0) + of(v, 16)) + (of(v, 32) + of(v, 48));
 }
 
 // The gradient of combine: TPR threads (a wave, four tokens a workgroup, or all 256) take one token, hold
-// NV chunks of D each in registers and meet for the dot products, wave by wave in a fixed order.
-template <int DT, int TPR, int NV>
+// NV chunks of D each in registers, take J rows together and meet for the dot products, wave by wave in
+// a fixed order, for MEET pairs at a time.
+template <int DT, int TPR, int NV, int J>
 __global__ __launch_bounds__(256) void combine_grad_kernel(RowGradArgs p, int64_t first) {
-  constexpr int ES = DTypeInfo<DT>::bytes, CE = 16 / ES;
-  __shared__ float part[4];
+  constexpr int ES = DTypeInfo<DT>::bytes, CE = 16 / ES, MEET = 8;
+  static_assert(MEET % J == 0, "whole batches");
+  __shared__ float part[4][MEET];
   const int tid = threadIdx.x, i = tid % TPR;
-  const int64_t t = (first + blockIdx.x) * (256 / TPR) + tid / TPR;
+  const int64_t t = (first + blockIdx.x) * (256 / TPR) + (TPR == 64 ? __builtin_amdgcn_readfirstlane(tid >> 6) : 0);
   if (TPR == 64 && t >= p.T) return;
   const int64_t chunks = ((int64_t)p.K * ES + 15) / 16;
   const uint8_t* const D = reinterpret_cast<const uint8_t*>(p.D) + t * p.ldd * ES;
@@ -144,60 +172,95 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowGradArgs p, int64_
 #pragma unroll
   for (int u = 0; u < NV; ++u)
     if (i + u * TPR < chunks) d[u] = load_chunk<ES>(D, i + u * TPR, p.K);
-  for (int j = 0; j < p.top; ++j) {
-    const int64_t pair = t * p.top + j;
-    const int at = p.place[pair];
-    if (at < 0 || at >= p.R) {
-      if (i == 0) p.dw[pair] = 0.0f;
-      continue;
-    }
-    const float w = p.weight[pair];
-    const uint8_t* const Y = reinterpret_cast<const uint8_t*>(p.Y) + at * p.ldy * ES;
-    uint8_t* const dY = reinterpret_cast<uint8_t*>(p.dY) + at * p.lddy * ES;
-    float dot = 0.0f;
-    auto chunk = [&](int64_t c, m_u32x4 dv, m_u32x4 yv) {
+  for (int j = 0; j < p.top; j += J) {
+    const Pairs<J> pairs(p.place, p.weight, t * p.top, j, p.top, p.R);
+    float dot[J] = {};
+    auto chunk = [&](int q, int64_t c, m_u32x4 dv, m_u32x4 yv) {
       float o[CE];
 #pragma unroll
       for (int e = 0; e < CE; ++e) {
         const float x = element<DT>(dv, e);
-        dot = fmaf(x, element<DT>(yv, e), dot);
-        o[e] = w * x;
+        dot[q] = fmaf(x, element<DT>(yv, e), dot[q]);
+        o[e] = pairs.w[q] * x;
       }
-      store_chunk<ES>(dY, c, p.K, pack<DT>(o));
+      store_chunk<ES>(reinterpret_cast<uint8_t*>(p.dY) + pairs.at[q] * p.lddy * ES, c, p.K, pack<DT>(o));
     };
-    m_u32x4 y[NV];
+    if (p.R > 0) {
+      m_u32x4 y[J][NV];
 #pragma unroll
-    for (int u = 0; u < NV; ++u)
-      if (i + u * TPR < chunks) y[u] = load_chunk<ES>(Y, i + u * TPR, p.K);
+      for (int q = 0; q < J; ++q)
 #pragma unroll
-    for (int u = 0; u < NV; ++u)
-      if (i + u * TPR < chunks) chunk(i + u * TPR, d[u], y[u]);
-    for (int64_t c = i + NV * TPR; c < chunks; c += TPR) chunk(c, load_chunk<ES>(D, c, p.K), load_chunk<ES>(Y, c, p.K));
+        for (int u = 0; u < NV; ++u)
+          if (i + u * TPR < chunks)
+            y[q][u] = load_chunk<ES>(reinterpret_cast<const uint8_t*>(p.Y) + pairs.at[q] * p.ldy * ES, i + u * TPR, p.K);
 #pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) dot += __shfl_xor(dot, s);
-    if constexpr (TPR > 64) {
-      __syncthreads();
-      if ((tid & 63) == 0) part[tid >> 6] = dot;
-      __syncthreads();
-      dot = (part[0] + part[1]) + (part[2] + part[3]);
+      for (int q = 0; q < J; ++q) {
+        if (!pairs.ok[q]) continue;
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+          if (i + u * TPR < chunks) chunk(q, i + u * TPR, d[u], y[q][u]);
+        const uint8_t* const Y = reinterpret_cast<const uint8_t*>(p.Y) + pairs.at[q] * p.ldy * ES;
+        for (int64_t c = i + NV * TPR; c < chunks; c += TPR) chunk(q, c, load_chunk<ES>(D, c, p.K), load_chunk<ES>(Y, c, p.K));
+      }
     }
-    if (i == 0) p.dw[pair] = dot;
+#pragma unroll
+    for (int q = 0; q < J; ++q) {
+      const float s = wave_sum(dot[q]);
+      if constexpr (TPR == 64) {
+        if (i == 0 && j + q < p.top) p.dw[t * p.top + j + q] = s;
+      } else if ((tid & 63) == 0) {
+        part[tid >> 6][(j + q) % MEET] = s;
+      }
+    }
+    if constexpr (TPR > 64) {
+      if ((j + J) % MEET == 0 || j + J >= p.top) {
+        __syncthreads();
+        const int from = j / MEET * MEET;
+        if (tid < MEET && from + tid < p.top)
+          p.dw[t * p.top + from + tid] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+        __syncthreads();
+      }
+    }
   }
 }
 
-template <int DT, int TPR, int NV>
+template <int DT, int TPR, int NV, int J>
 hipError_t grad_cfg(const RowGradArgs& p, hipStream_t s) {
   constexpr int RPW = 256 / TPR;
   return launch_in_slices(((int64_t)p.T + RPW - 1) / RPW, 256, [&](int64_t first, unsigned n) {
-    hipLaunchKernelGGL((combine_grad_kernel<DT, TPR, NV>), dim3(n), dim3(256), 0, s, p, first);
+    hipLaunchKernelGGL((combine_grad_kernel<DT, TPR, NV, J>), dim3(n), dim3(256), 0, s, p, first);
   });
 }
 
+// A wave is enough for a row of 2 KB and spares the meeting (8192 tokens of 4 x 1024: 33.2 us against 46.2,
+// 16384 of 8 x 512: 61.8 against 127.4); of longer rows a wave takes too long over one token (8190 of 8 x
+// 2048: 129.2 against 117.5; 512 of 8 x 4096: 34.4 against 13.5).  Two chunks a thread, four where the row has
+// them (4096 of 8 x 7168: 205 us against 216).  Two pairs together, unless there is one alone (8192 of 1 x
+// 4096: 34.0 us against 38.5 with a second that is none).
+template <int DT, int J>
+hipError_t grad_pairs(const RowGradArgs& p, hipStream_t s) {
+  const int64_t chunks = ((int64_t)p.K * DTypeInfo<DT>::bytes + 15) / 16;
+  if (chunks <= 64 * 2) return grad_cfg<DT, 64, 2, J>(p, s);
+  if (chunks <= 256 * 2) return grad_cfg<DT, 256, 2, J>(p, s);
+  return grad_cfg<DT, 256, 4, J>(p, s);
+}
 template <int DT>
 hipError_t grad_type(const RowGradArgs& p, hipStream_t s) {
-  const int64_t chunks = ((int64_t)p.K * DTypeInfo<DT>::bytes + 15) / 16;
-  if (chunks <= 64 * 4) return grad_cfg<DT, 64, 4>(p, s);
-  return grad_cfg<DT, 256, 4>(p, s);
+  return p.top == 1 ? grad_pairs<DT, 1>(p, s) : grad_pairs<DT, 2>(p, s);
+}
+
+// Two pairs together as well (8192 tokens of 1 x 4096: 27.0 us with one, 30.2 with two; 4096 of 2 x 4096: 20.3
+// and 19.4; more gain nothing for 8 pairs and cost for fewer).
+template <int DT, int J>
+hipError_t combine_cfg(const RowArgs& p, hipStream_t s) {
+  const int64_t per = pieces(p.K, DTypeInfo<DT>::bytes);
+  return launch_in_slices((p.T * per + 3) / 4, 256, [&](int64_t first, unsigned n) {
+    hipLaunchKernelGGL((combine_kernel<DT, J>), dim3(n), dim3(256), 0, s, p, first, (int)per);
+  });
+}
+template <int DT>
+hipError_t combine_type(const RowArgs& p, hipStream_t s) {
+  return p.top == 1 ? combine_cfg<DT, 1>(p, s) : combine_cfg<DT, 2>(p, s);
 }
 
 }  // namespace
@@ -211,12 +274,7 @@ hipError_t launch_dispatch_rows(const RowArgs& p, int type, hipStream_t s) {
 }
 
 hipError_t launch_combine_rows(const RowArgs& p, int type, hipStream_t s) {
-  const int64_t per = pieces(p.K, type == F32 ? 4 : 2);
-  return launch_in_slices((p.T * per + 3) / 4, 256, [&](int64_t first, unsigned n) {
-    if (type == F32) hipLaunchKernelGGL((combine_kernel<F32>), dim3(n), dim3(256), 0, s, p, first, (int)per);
-    else if (type == F16) hipLaunchKernelGGL((combine_kernel<F16>), dim3(n), dim3(256), 0, s, p, first, (int)per);
-    else hipLaunchKernelGGL((combine_kernel<BF16>), dim3(n), dim3(256), 0, s, p, first, (int)per);
-  });
+  return type == F32 ? combine_type<F32>(p, s) : type == F16 ? combine_type<F16>(p, s) : combine_type<BF16>(p, s);
 }
 
 hipError_t launch_combine_rows_grad(const RowGradArgs& p, int type, hipStream_t s) {
