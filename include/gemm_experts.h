@@ -85,7 +85,9 @@ GEMM_API gemm_status_t gemm_route(gemm_handle_t h, void* stream, int64_t tokens,
  * logits, score, renorm and scale as gemm_route was given them, expert as it wrote them (the experts of
  * a token are distinct; -1 and any other number that is no expert is skipped); dweight fp32, tokens x
  * top; dlogits: tokens x experts (ldd >= experts) of x_type, computed in fp32 and rounded once.  Every
- * element is written.  A logit of -infinity has gradient 0.  Errors as gemm_route. */
+ * element is written.  A logit of -infinity has gradient 0, also where all of a token's are
+ * (but a NaN or +infinity among a softmax's logits makes all of the token's gradients NaN).  Errors as
+ * gemm_route. */
 GEMM_API gemm_status_t gemm_route_grad(gemm_handle_t h, void* stream, int64_t tokens, int64_t experts,
                                        int64_t top, const void* logits, int64_t ldl, gemm_dtype_t x_type,
                                        gemm_score_t score, int renorm, float scale,
@@ -94,8 +96,8 @@ GEMM_API gemm_status_t gemm_route_grad(gemm_handle_t h, void* stream, int64_t to
 
 /* Rows to the experts: A[place[t * top + j]] = X[t], for all j < top.
  * X is tokens x K (ldx >= K), A rows x K (lda >= K), both of type GEMM_F32, GEMM_F16 or GEMM_BF16.
- * A place outside 0 .. rows - 1 is skipped; rows of A that no pair has are left as they were; a place
- * that comes twice holds one of its rows.  top >= 1, rows >= 0. */
+ * A place outside 0 .. rows - 1 is skipped; rows of A that no pair has are left as they were.  Places
+ * are distinct (gemm_route's are): a row that has two pairs holds parts of either's.  top >= 1, rows >= 0. */
 GEMM_API gemm_status_t gemm_dispatch_rows(gemm_handle_t h, void* stream, int64_t tokens, int64_t top,
                                           int64_t K, const void* X, int64_t ldx, gemm_dtype_t type,
                                           const int32_t* place, int64_t rows, void* A, int64_t lda);
@@ -117,8 +119,8 @@ GEMM_API gemm_status_t gemm_combine_rows(gemm_handle_t h, void* stream, int64_t 
  *     dY[place[t * top + j]]  = weight[t * top + j] * D[t]                      (rows x K, lddy >= K)
  *     dweight[t * top + j]    = sum over k of D[t][k] * Y[place[t * top + j]][k]         (fp32)
  *
- * A skipped place has dweight 0; rows of dY that no pair has are left as they were.  dweight's sums are
- * fp32, in an order that depends on K only. */
+ * A skipped place has dweight 0; rows of dY that no pair has are left as they were; places are distinct, as
+ * for gemm_dispatch_rows.  dweight's sums are fp32, in an order that depends on K only. */
 GEMM_API gemm_status_t gemm_combine_rows_grad(gemm_handle_t h, void* stream, int64_t tokens, int64_t top,
                                               int64_t K, const void* D, int64_t ldd, const void* Y,
                                               int64_t ldy, gemm_dtype_t type, const int32_t* place,
@@ -138,7 +140,7 @@ GEMM_API gemm_status_t gemm_combine_rows_grad(gemm_handle_t h, void* stream, int
  * X is M x K (ldx >= K) of x_type GEMM_F32, GEMM_F16 or GEMM_BF16, K a multiple of 32; q_type is
  * GEMM_E2M1: Q has rows of ldq elements (two a byte, ldq even and at least K), S rows of lds >= K / 32
  * bytes.  With place NULL row i goes to row i (top 1, rows = M); with place (M x top, as gemm_route
- * writes it) to the rows place[i * top + j], as gemm_dispatch_rows would send it. */
+ * writes it) to the rows place[i * top + j], as gemm_dispatch_rows would send it (distinct, too). */
 GEMM_API gemm_status_t gemm_quantize_mx(gemm_handle_t h, void* stream, int64_t M, int64_t K,
                                         const void* X, int64_t ldx, gemm_dtype_t x_type, int64_t top,
                                         const int32_t* place, int64_t rows, void* Q, int64_t ldq,

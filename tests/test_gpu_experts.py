@@ -392,6 +392,27 @@ def test_route_grad_of_a_weight_near_one(g):
         assert (np.abs(got - ref)[:, 5] <= 400 * U32 * np.abs(ref[:, 5])).all()
 
 
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_route_grad_of_masked_tokens(g, kind, renorm):
+    """Tokens without any logit, with one, and with none but those that were not chosen: no NaN."""
+    for E, k in ((5, 2), (60, 4), (256, 8), (300, 20)):
+        x = logits(6, E, E)
+        expert = np.argsort(RNG(E).random((6, E)), axis=1)[:, :k]
+        x[0] = x[1] = x[5] = -INF
+        expert[0] = -1                                    # as the router answers; token 1 names experts all the same
+        x[2, 1:] = -INF
+        expert[2], expert[2, 0] = -1, 0
+        expert[3] = -1
+        dw = RNG(7).standard_normal((6, k)).astype(np.float32).astype(np.float64)
+        got, xr = call_grad(g, x, expert, dw, "f32", kind, renorm, 1.5)
+        assert (got[[0, 1, 3, 5]] == 0).all()
+        keep = [2, 4]
+        with np.errstate(invalid="ignore"):
+            ref, den = grad_reference(xr[keep], expert[keep], dw[keep], kind, renorm, 1.5)
+        check(got[keep], ref, 148 * U32 * den, "f32", (E, k))
+
+
 def test_route_grad_skips_what_is_no_expert(g):
     x = logits(4, 10, 1)
     expert = np.array([[1, 2], [-1, 3], [10, 4], [2 ** 31 - 1, -2 ** 31]])
@@ -822,6 +843,33 @@ def test_mx_nan_scales_stay_in_their_rows(g, kernel):
     assert torch.equal(bad, want)
 
 
+@pytest.mark.parametrize("kernel", [STREAM] + TILES)
+def test_mx_far_addresses(g, kernel):
+    """Rows of A, their results and a group's matrix further than 2^32 bytes from the start."""
+    import torch
+    M, N, K, ld, ldc = 530, 40, 64, 2 ** 24, 2 ** 23
+    rng = RNG([kernel, 77])
+    qa, sa, a = random_mx(rng, M, K, K, 16)
+    qb, sb, b = random_mx(rng, 2 * N, K, K, 16)
+    A = torch.zeros(M, ld // 2, dtype=torch.uint8, device="cuda:0")         # 4.4 GB
+    A[:, :K // 2] = torch.from_numpy(qa).cuda()
+    far = 2 ** 32 + 4096
+    B = torch.zeros(far + N * K, dtype=torch.uint8, device="cuda:0")
+    for i in range(2):
+        B[i * far:i * far + N * K // 2] = torch.from_numpy(qb[i * N:(i + 1) * N].ravel()).cuda()
+    C = torch.zeros(M, ldc, dtype=torch.bfloat16, device="cuda:0")           # 8.9 GB
+    off = dev(np.array([0, 3, M], dtype=np.int64))
+    SA, SB = torch.from_numpy(sa).cuda(), torch.from_numpy(sb).cuda()
+    g.run_grouped_mx(A, SA, B, SB, C, off, groups=2, M=M, N=N, K=K, lda=ld, ldsa=16, ldsb=16, stride_b=2 * far,
+                     stride_sb=16 * N, ldc=ldc, kernel=kernel)
+    torch.cuda.synchronize()
+    w = [b[:N], b[N:]]
+    ref = np.concatenate([a[:3] @ w[0].T, a[3:] @ w[1].T])
+    D = np.concatenate([np.abs(a[:3]) @ np.abs(w[0]).T, np.abs(a[3:]) @ np.abs(w[1]).T])
+    check(host(C[:, :N].contiguous()), ref, (K * 2.0 ** -23 + HALF_STEP["bf16"] + 4 * U32) * D, "bf16", kernel)
+    assert not C[:, N:N + 64].any() and not C[:, ldc - 64:].any()
+
+
 def test_mx_refuses_what_a_kernel_cannot(g):
     import torch
     import tiled_matrix_multiply_amd as tmm
@@ -959,6 +1007,54 @@ def test_layer_in_a_graph(g, n):
         torch.cuda.synchronize()
         for name in ("expert", "weight", "place", "offsets", "out"):
             assert torch.equal(bufs[name], other[-1][name]), (i, name)
+
+
+@pytest.mark.parametrize("n", [3, 130])
+def test_training_step_in_a_graph(g, n):
+    """The router and the rows' ways there and back with all their gradients, captured, and replayed with
+    other tokens and eager work between: every replay equals the eager result."""
+    import torch
+    import tiled_matrix_multiply_amd as tmm
+    E, k, K = 12, 3, 520
+    R = n * k
+    ws = torch.zeros(max(16, tmm.route_workspace_bytes(n, E)), dtype=torch.uint8, device="cuda:0")
+
+    def make():
+        i32 = [torch.empty(n, k, dtype=torch.int32, device="cuda:0") for _ in range(2)]
+        f32 = [torch.empty(n, k, device="cuda:0") for _ in range(2)]
+        rows = [torch.zeros(R, K, device="cuda:0", dtype=torch.bfloat16) for _ in range(2)]
+        return dict(x=torch.zeros(n, K, device="cuda:0", dtype=torch.bfloat16), lg=torch.zeros(n, E, device="cuda:0"),
+                    d=torch.zeros(n, K, device="cuda:0", dtype=torch.bfloat16), expert=i32[0], place=i32[1], w=f32[0],
+                    dw=f32[1], a=rows[0], dy=rows[1], off=torch.empty(E + 1, dtype=torch.int64, device="cuda:0"),
+                    out=torch.empty(n, K, device="cuda:0", dtype=torch.bfloat16),
+                    dx=torch.empty(n, K, device="cuda:0", dtype=torch.bfloat16), dl=torch.empty(n, E, device="cuda:0"))
+
+    def step(b):
+        kw = dict(tokens=n, top=k, K=K, rows=R)
+        g.route(b["lg"], b["expert"], b["w"], b["place"], b["off"], tokens=n, experts=E, top=k, workspace=ws)
+        g.dispatch_rows(b["x"], b["place"], b["a"], **kw)
+        g.combine_rows(b["a"], b["place"], b["out"], weight=b["w"], **kw)
+        g.combine_rows_grad(b["d"], b["a"], b["place"], b["w"], b["dy"], b["dw"], **kw)
+        g.combine_rows(b["dy"], b["place"], b["dx"], **kw)
+        g.route_grad(b["lg"], b["expert"], b["dw"], b["dl"], tokens=n, experts=E, top=k)
+
+    b, eager = make(), make()
+    step(b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(b)
+    for i in range(4):
+        gen = torch.Generator(device="cuda:0").manual_seed(i)
+        for name in ("x", "lg", "d"):
+            b[name].copy_(torch.randn(b[name].shape, device="cuda:0", generator=gen))
+            eager[name].copy_(b[name])
+        step(eager)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for name in b:
+            assert torch.equal(b[name], eager[name]), (i, name)
 
 
 def test_two_streams_at_once(g):

@@ -843,11 +843,10 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
   if (sub < p.top) {
     e = p.expert[tt * p.top + sub];
     g = p.scale * p.dw[tt * p.top + sub];
-    if (e < 0 || e >= p.E) {
+    if (e >= 0 && e < p.E) cx = load_logit(p.x, tt * p.ldx + e, p.x_type);
+    if (cx == kNone) {  // no expert, or none that could be chosen
       e = -1;
       g = 0.0f;
-    } else {
-      cx = load_logit(p.x, tt * p.ldx + e, p.x_type);
     }
   }
   const int e0 = sub * V, n = min(max(p.E - e0, 0), V);
@@ -860,7 +859,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = v[i] == kNone ? 0.0f : exp_near(v[i] - x_max);
     sum = sum_across<L>(lane_sum<V>(v));
-    const float r = 1.0f / sum;
+    const float r = sum == 0.0f ? 0.0f : 1.0f / sum;  // (a token that is masked as a whole)
 #pragma unroll
     for (int i = 0; i < V; ++i) mine[e0 + i] = v[i] * r;
     row_written();
@@ -904,7 +903,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
 #pragma unroll
   for (int i = 0; i < V; ++i) mine[e0 + i] = full ? -v[i] * dot : 0.0f;
   row_written();
-  if (e >= 0) mine[e] = cx == kNone ? 0.0f : d;
+  if (e >= 0) mine[e] = d;
   row_written();
   if (!live) return;
 #pragma unroll
