@@ -64,8 +64,7 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(GemmParams p, GroupA
   }
 
   // What the thread finishes at the end: items of four columns, and their bias, which would otherwise come in
-  // after the sums, with nothing left to hide its way from memory (32 rows over 64 groups of 1024 x 2048 with
-  // bias and GELU FIGB).
+  // after the sums, with nothing left to hide its way from memory.
   constexpr int ITEMS = NF * MF * 64, MINE = (ITEMS + 64 * NW - 1) / (64 * NW);
   auto item = [&](int i, int& m, int& n) {
     m = m0 + 16 * ((i >> 6) % MF) + (i & 15);

@@ -290,8 +290,10 @@ gemm_status_t run(gemm_handle_t h, gemm_grouped_kernel_t kernel, void* stream, c
     // the columns where that is not one each (1 x 4096 x 4096 4.0 against 5.2, 16 x 8192 x 4096, two each, 7.4 against
     // 6.5) or rows weigh little: twice as many workgroups even out the last round (1 x 20480 x 7168 14.3 against
     // 15.7, 1 x 16384 x 7168, two each exactly, 12.1 against 11.4).
+    // (No more than there are: a group of several may have twice the average.)
+    const int64_t most = a.groups == 1 ? a.M : 2 * average_rows(a);
     int rows = 16;
-    while (rows < 64 && rows < 2 * average_rows(a) && 10 * expected_tiles(a, rows, 32) > 16 * h->cu_count) rows *= 2;
+    while (rows < 64 && rows < most && 10 * expected_tiles(a, rows, 32) > 16 * h->cu_count) rows *= 2;
     while (rows < 64 && !countable(a, rows, 32)) rows *= 2;
     const bool narrow = rows == 16 && countable(a, 16, 16) &&
                         ((a.groups == 1 && a.M <= 8) || expected_tiles(a, 16, 16) <= h->cu_count);
