@@ -567,6 +567,52 @@ def test_rows_far_addresses(g):
         assert torch.equal(Q[r * 8192:r * 8192 + K // 2], q1[t]) and torch.equal(S[r, :3], s1[t])
 
 
+@pytest.mark.parametrize("t,n,k,K,ld", [("bf16", 1601, 8, 2051, 2053), ("bf16", 8200, 8, 2056, 2056),
+                                        ("f16", 30001, 1, 1001, 1002), ("f32", 4099, 3, 5600, 5600),
+                                        ("f32", 16500, 2, 2052, 2053)])
+def test_rows_past_the_caches(g, t, n, k, K, ld):
+    """Rows of more than 48 and 256 MB, which take loads and stores that are not kept: dispatch exactly, the
+    sums of at most 8 and K products in fp32 with one rounding."""
+    import torch
+    gen = torch.Generator(device="cuda:0").manual_seed(n)
+    R = n * k
+    place = torch.randperm(R, device="cuda:0", generator=gen).view(n, k)
+    place[5] = -1
+    X, Y, A, dY = (torch.randn(rows, ld, device="cuda:0", generator=gen).to(T()[t]) for rows in (n, R, R, R))
+    C, w = torch.randn(n, ld, device="cuda:0", generator=gen).to(T()[t]), torch.rand(n, k, device="cuda:0", generator=gen)
+    dw, before = torch.empty(n, k, device="cuda:0"), (A.clone(), C.clone(), dY.clone())
+    p32, kw = place.int(), dict(tokens=n, top=k, K=K, rows=R, dtype=t)
+    g.dispatch_rows(X, p32, A, ldx=ld, lda=ld, **kw)
+    g.combine_rows(Y, p32, C, weight=w, beta=0.5, ldy=ld, ldc=ld, **kw)
+    g.combine_rows_grad(X, Y, p32, w, dY, dw, ldd=ld, ldy=ld, lddy=ld, **kw)
+    torch.cuda.synchronize()
+    live = place >= 0
+    at, tok = place[live], torch.arange(n, device="cuda:0")[:, None].expand(n, k)[live]
+    want = before[0].clone()
+    want[at, :K] = X[tok, :K]
+    assert torch.equal(bits(A), bits(want))
+    # a product, rounded to fp32 (or, where the compiler joins the product and the conversion, not) and then
+    # to the type: within half a step of the type plus one of fp32 of the exact product, and of a subnormal
+    # result within half the type's smallest number
+    exact = w[live][:, None].double() * X[tok, :K].double()
+    off = (dY[at, :K].double() - exact).abs()
+    assert (off <= (HALF_STEP[t] + 1.01 * U32) * exact.abs() + TINY[t]).all()
+    dY[at, :K] = before[2][at, :K]
+    assert torch.equal(bits(dY), bits(before[2]))
+    assert torch.equal(bits(C[:, K:]), bits(before[1][:, K:])) and (dw[5] == 0).all()
+    x, h = X[:, :K].double(), HALF_STEP[t]
+    ref, den = 0.5 * before[1][:, :K].double(), 0.5 * before[1][:, :K].double().abs()
+    for j in range(k):
+        y = torch.where(live[:, j, None], Y[place[:, j].clamp_min(0), :K].double(), 0.0)
+        ref += w[:, j, None].double() * y
+        den += w[:, j, None].double() * y.abs()
+        dot, size = (x * y).sum(dim=1), (x * y).abs().sum(dim=1)
+        assert ((dw[:, j].double() - dot).abs() <= (K + 2) * U32 * size).all()
+    # (fp16's subnormal numbers lie 2^-24 apart: half of that, TINY, is the least that a rounding is off by)
+    lim = (k + 1) * U32 * den + h * (ref.abs() + (k + 1) * U32 * den) + TINY[t]
+    assert ((C[:, :K].double() - ref).abs() <= lim).all()
+
+
 # ---------------------------------------------------------------------------- quantize_mx --
 
 GRID = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])

@@ -3,7 +3,7 @@
 // Everything goes by tokens: the places of a token's pairs are a few neighbouring numbers, a token's row
 // is read (or written) once, and the experts' rows are whole rows, so that each 16-byte access of a wave
 // lies in one run of 1 KB whatever the order.  What bounds it is the bytes: 8190 tokens of 8 x 2048 in bf16
-// dispatched in 58.5 us (5.16 TB/s), combined in 60.4 (5.00), the gradient 117.4 (4.86), where a copy of
+// dispatched in 58.8 us (5.13 TB/s), combined in 51.3 (5.88), the gradient 118.2 (4.82), where a copy of
 // 4 GiB runs at 4.63.
 #include <type_traits>
 
@@ -14,15 +14,17 @@ namespace tgemm {
 namespace {
 
 typedef uint32_t m_u32x4 __attribute__((ext_vector_type(4)));
+typedef m_u32x4 m_any4 __attribute__((aligned(2)));
 
-// Chunk c (16 bytes) of a row of K elements, zeros past its end; any alignment.
-template <int ES>
+// Chunk c (16 bytes) of a row of K elements, zeros past its end; any alignment.  NT: not kept in the caches.
+template <int ES, bool NT = false>
 __device__ __forceinline__ m_u32x4 load_chunk(const uint8_t* row, int64_t c, int K) {
   constexpr int CE = 16 / ES;
   m_u32x4 v = m_u32x4{0u, 0u, 0u, 0u};
   const int64_t k = c * CE;
   if (k + CE <= K) {
-    __builtin_memcpy(&v, row + k * ES, 16);
+    if constexpr (NT) v = __builtin_nontemporal_load(reinterpret_cast<const m_any4*>(row + k * ES));
+    else __builtin_memcpy(&v, row + k * ES, 16);
   } else {
     for (int e = 0; e < CE; ++e)
       if (k + e < K) {
@@ -33,12 +35,13 @@ __device__ __forceinline__ m_u32x4 load_chunk(const uint8_t* row, int64_t c, int
   return v;
 }
 
-template <int ES>
+template <int ES, bool NT = false>
 __device__ __forceinline__ void store_chunk(uint8_t* row, int64_t c, int K, m_u32x4 v) {
   constexpr int CE = 16 / ES;
   const int64_t k = c * CE;
   if (k + CE <= K) {
-    __builtin_memcpy(row + k * ES, &v, 16);
+    if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<m_any4*>(row + k * ES));
+    else __builtin_memcpy(row + k * ES, &v, 16);
   } else {
     for (int e = 0; e < CE; ++e)
       if (k + e < K) {
@@ -83,7 +86,7 @@ struct Piece {
   }
 };
 
-template <int ES>
+template <int ES, bool NT>
 __global__ __launch_bounds__(256) void dispatch_kernel(RowArgs p, int64_t first, int per) {
   const Piece at(first, per);
   if (at.t >= p.T || at.c * (16 / ES) >= p.K) return;
@@ -91,7 +94,7 @@ __global__ __launch_bounds__(256) void dispatch_kernel(RowArgs p, int64_t first,
   for (int j = 0; j < p.top; ++j) {
     const int row = p.place[at.t * p.top + j];
     if (row < 0 || row >= p.R) continue;
-    store_chunk<ES>(reinterpret_cast<uint8_t*>(p.Y) + row * p.ldy * ES, at.c, p.K, v);
+    store_chunk<ES, NT>(reinterpret_cast<uint8_t*>(p.Y) + row * p.ldy * ES, at.c, p.K, v);
   }
 }
 
@@ -114,7 +117,7 @@ struct Pairs {
   }
 };
 
-template <int DT, int J>
+template <int DT, int J, bool NT>
 __global__ __launch_bounds__(256) void combine_kernel(RowArgs p, int64_t first, int per) {
   constexpr int ES = DTypeInfo<DT>::bytes, CE = 16 / ES;
   const Piece at(first, per);
@@ -125,7 +128,7 @@ __global__ __launch_bounds__(256) void combine_kernel(RowArgs p, int64_t first, 
     m_u32x4 v[J];
 #pragma unroll
     for (int q = 0; q < J; ++q)
-      v[q] = load_chunk<ES>(reinterpret_cast<const uint8_t*>(p.X) + pairs.at[q] * p.ldx * ES, at.c, p.K);
+      v[q] = load_chunk<ES, NT>(reinterpret_cast<const uint8_t*>(p.X) + pairs.at[q] * p.ldx * ES, at.c, p.K);
 #pragma unroll
     for (int q = 0; q < J; ++q) {
       if (!pairs.ok[q]) continue;
@@ -139,7 +142,7 @@ __global__ __launch_bounds__(256) void combine_kernel(RowArgs p, int64_t first, 
 #pragma unroll
     for (int e = 0; e < CE; ++e) sum[e] = fmaf(p.beta, element<DT>(c, e), sum[e]);
   }
-  store_chunk<ES>(dst, at.c, p.K, pack<DT>(sum));
+  store_chunk<ES, NT>(dst, at.c, p.K, pack<DT>(sum));
 }
 
 // The sum over a wave, in every lane, in a fixed order.
@@ -158,7 +161,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 // The gradient of combine: TPR threads (a wave, four tokens a workgroup, or all 256) take one token, hold
 // NV chunks of D each in registers, take J rows together and meet for the dot products, wave by wave in
 // a fixed order, for MEET pairs at a time.
-template <int DT, int TPR, int NV, int J>
+template <int DT, int TPR, int NV, int J, bool NT>
 __global__ __launch_bounds__(256) void combine_grad_kernel(RowGradArgs p, int64_t first) {
   constexpr int ES = DTypeInfo<DT>::bytes, CE = 16 / ES, MEET = 8;
   static_assert(MEET % J == 0, "whole batches");
@@ -171,7 +174,7 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowGradArgs p, int64_
   m_u32x4 d[NV];
 #pragma unroll
   for (int u = 0; u < NV; ++u)
-    if (i + u * TPR < chunks) d[u] = load_chunk<ES>(D, i + u * TPR, p.K);
+    if (i + u * TPR < chunks) d[u] = load_chunk<ES, NT>(D, i + u * TPR, p.K);
   for (int j = 0; j < p.top; j += J) {
     const Pairs<J> pairs(p.place, p.weight, t * p.top, j, p.top, p.R);
     float dot[J] = {};
@@ -192,7 +195,8 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowGradArgs p, int64_
 #pragma unroll
         for (int u = 0; u < NV; ++u)
           if (i + u * TPR < chunks)
-            y[q][u] = load_chunk<ES>(reinterpret_cast<const uint8_t*>(p.Y) + pairs.at[q] * p.ldy * ES, i + u * TPR, p.K);
+            y[q][u] =
+                load_chunk<ES, NT>(reinterpret_cast<const uint8_t*>(p.Y) + pairs.at[q] * p.ldy * ES, i + u * TPR, p.K);
 #pragma unroll
       for (int q = 0; q < J; ++q) {
         if (!pairs.ok[q]) continue;
@@ -224,11 +228,26 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowGradArgs p, int64_
   }
 }
 
+// What the caches are not to keep.  The memory-side cache holds 256 MB, and a call's rows push out of it what
+// the next call could have read there: rows that are read for the last time (combine and its gradient) and
+// the sums of many go past it.  8190 tokens dispatched to 8 rows of 2048 and others combined: 139.5 us with
+// ordinary accesses, 108.3 so; 4096 to 2 of 4096, both ways with all gradients: 85.5 and 83.6, 16384 to 2: 372
+// and 324; but 512 to 8 of 4096, 34 MB of rows, which stay there from call to call: 37.4 and 40.6.  Dispatched
+// rows are read next, so they go past it only where it could not hold them (16384 to 2 of 4096, 268 MB,
+// dispatched and others combined: 143.9 us with ordinary stores, 125.9 so, and the same for the same rows; 8190 to
+// 8 of 2048, the same rows combined: 90.7 and 103.8).
+inline bool past_caches(int64_t T, int64_t top, int64_t K, int es, int64_t bytes) {
+  return (__int128)(T * top) * K * es >= bytes;
+}
+constexpr int64_t kReadOnce = int64_t(48) << 20, kTooLarge = int64_t(256) << 20;
+
 template <int DT, int TPR, int NV, int J>
 hipError_t grad_cfg(const RowGradArgs& p, hipStream_t s) {
   constexpr int RPW = 256 / TPR;
+  const bool nt = past_caches(p.T, p.top, p.K, DTypeInfo<DT>::bytes, kReadOnce);
   return launch_in_slices(((int64_t)p.T + RPW - 1) / RPW, 256, [&](int64_t first, unsigned n) {
-    hipLaunchKernelGGL((combine_grad_kernel<DT, TPR, NV, J>), dim3(n), dim3(256), 0, s, p, first);
+    if (nt) hipLaunchKernelGGL((combine_grad_kernel<DT, TPR, NV, J, true>), dim3(n), dim3(256), 0, s, p, first);
+    else hipLaunchKernelGGL((combine_grad_kernel<DT, TPR, NV, J, false>), dim3(n), dim3(256), 0, s, p, first);
   });
 }
 
@@ -254,8 +273,10 @@ hipError_t grad_type(const RowGradArgs& p, hipStream_t s) {
 template <int DT, int J>
 hipError_t combine_cfg(const RowArgs& p, hipStream_t s) {
   const int64_t per = pieces(p.K, DTypeInfo<DT>::bytes);
+  const bool nt = past_caches(p.T, p.top, p.K, DTypeInfo<DT>::bytes, kReadOnce);
   return launch_in_slices((p.T * per + 3) / 4, 256, [&](int64_t first, unsigned n) {
-    hipLaunchKernelGGL((combine_kernel<DT, J>), dim3(n), dim3(256), 0, s, p, first, (int)per);
+    if (nt) hipLaunchKernelGGL((combine_kernel<DT, J, true>), dim3(n), dim3(256), 0, s, p, first, (int)per);
+    else hipLaunchKernelGGL((combine_kernel<DT, J, false>), dim3(n), dim3(256), 0, s, p, first, (int)per);
   });
 }
 template <int DT>
@@ -263,14 +284,20 @@ hipError_t combine_type(const RowArgs& p, hipStream_t s) {
   return p.top == 1 ? combine_cfg<DT, 1>(p, s) : combine_cfg<DT, 2>(p, s);
 }
 
+template <int ES, bool NT>
+hipError_t dispatch_cfg(const RowArgs& p, hipStream_t s) {
+  const int64_t per = pieces(p.K, ES);
+  return launch_in_slices((p.T * per + 3) / 4, 256, [&](int64_t first, unsigned n) {
+    hipLaunchKernelGGL((dispatch_kernel<ES, NT>), dim3(n), dim3(256), 0, s, p, first, (int)per);
+  });
+}
+
 }  // namespace
 
 hipError_t launch_dispatch_rows(const RowArgs& p, int type, hipStream_t s) {
-  const int64_t per = pieces(p.K, type == F32 ? 4 : 2);
-  return launch_in_slices((p.T * per + 3) / 4, 256, [&](int64_t first, unsigned n) {
-    if (type == F32) hipLaunchKernelGGL((dispatch_kernel<4>), dim3(n), dim3(256), 0, s, p, first, (int)per);
-    else hipLaunchKernelGGL((dispatch_kernel<2>), dim3(n), dim3(256), 0, s, p, first, (int)per);
-  });
+  const int es = type == F32 ? 4 : 2;
+  return past_caches(p.T, p.top, p.K, es, kTooLarge) ? (es == 4 ? dispatch_cfg<4, true>(p, s) : dispatch_cfg<2, true>(p, s))
+                                                     : (es == 4 ? dispatch_cfg<4, false>(p, s) : dispatch_cfg<2, false>(p, s));
 }
 
 hipError_t launch_combine_rows(const RowArgs& p, int type, hipStream_t s) {
