@@ -4,7 +4,7 @@
 // addresses that nothing dereferences.
 //
 // A line of input, one of
-//   mx kernel groups M N K lda ldb ldc ldsa ldsb stride skew c_type      (-1: the dense one)
+//   mx kernel groups M N K lda ldb ldc ldsa ldsb stride skew c_type epilogue   (-1: the dense one)
 //   moves T top K ld rows type          dispatch, combine, its gradient and quantization with places
 //   route T E top groups top_groups ldl type score renorm               and its gradient
 // skew: bytes that A starts after a multiple of 16.  A line of output: the statuses and launches.
@@ -56,9 +56,9 @@ int main() {
     launched.clear();
     if (!strcmp(call, "mx")) {
       long long G, M, N, K, lda, ldb, ldc, ldsa, ldsb, stride;
-      int kernel, skew, ct;
-      if (scanf("%d %lld %lld %lld %lld %lld %lld %lld %lld %lld %lld %d %d", &kernel, &G, &M, &N, &K, &lda, &ldb, &ldc,
-                &ldsa, &ldsb, &stride, &skew, &ct) != 13)
+      int kernel, skew, ct, epi;
+      if (scanf("%d %lld %lld %lld %lld %lld %lld %lld %lld %lld %lld %d %d %d", &kernel, &G, &M, &N, &K, &lda, &ldb, &ldc,
+                &ldsa, &ldsb, &stride, &skew, &ct, &epi) != 14)
         return 1;
       const long long blocks = (K / 32 + 15) / 16 * 16;
       if (lda < 0) lda = K;
@@ -70,7 +70,7 @@ int main() {
       const gemm_status_t st = gemm_run_grouped_mx(
           &h, (gemm_grouped_kernel_t)kernel, nullptr, G, (const int64_t*)far(1), M, N, K, 1.f, (uint8_t*)far(2) + skew, lda,
           (uint8_t*)far(3), ldsa, far(4), ldb, stride, (uint8_t*)far(5), ldsb, N * ldsb, 0.f, far(6), ldc, GEMM_E2M1,
-          (gemm_dtype_t)ct, 0, nullptr);
+          (gemm_dtype_t)ct, (uint32_t)epi, nullptr);
       printf("%d%s\n", (int)st, launched.c_str());
     } else if (!strcmp(call, "moves")) {
       long long T, top, K, ld, R;

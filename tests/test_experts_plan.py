@@ -41,8 +41,8 @@ def words(*args):
     return " ".join(str(a) for a in args)
 
 
-def mx(M, N, K, *, groups=1, kernel=0, lda=-1, ldb=-1, ldc=-1, ldsa=-1, ldsb=-1, stride=-1, skew=0, ct=BF16):
-    return words("mx", kernel, groups, M, N, K, lda, ldb, ldc, ldsa, ldsb, stride, skew, ct)
+def mx(M, N, K, *, groups=1, kernel=0, lda=-1, ldb=-1, ldc=-1, ldsa=-1, ldsb=-1, stride=-1, skew=0, ct=BF16, epi=0):
+    return words("mx", kernel, groups, M, N, K, lda, ldb, ldc, ldsa, ldsb, stride, skew, ct, epi)
 
 
 def stream(rows, columns):
@@ -57,26 +57,30 @@ def tile(n):
 # a third stage), 2 128 x 128, 3 256 x 256 mixed with 128 x 128
 @pytest.mark.parametrize("args,launch", [
     # one token up to eight stream whatever the width, in half as many columns
-    ((1, 65536, 2048, {}), stream(16, 16)), ((8, 65536, 2048, {}), stream(16, 16)), ((9, 65536, 2048, {}), tile(2)),
-    # up to 32 rows as long as 64 x 64 tiles are at most one and a half a compute unit
-    ((9, 24576, 2048, {}), stream(16, 32)), ((9, 24640, 2048, {}), tile(1)), ((9, 24640, 4096, {}), tile(4)),
-    ((32, 8192, 4096, {}), stream(32, 32)), ((33, 8192, 4096, {}), tile(4)),
-    # up to 128 as long as they are at most a quarter
-    ((128, 2048, 4096, {}), stream(32, 32)), ((128, 2112, 4096, {}), tile(4)), ((129, 1024, 4096, {}), tile(4)),
-    # the rows and columns of a streaming workgroup
-    ((16, 4096, 4096, {}), stream(16, 16)), ((16, 4112, 4096, {}), stream(16, 32)),
+    ((1, 65536, 2048, {}), stream(16, 16)), ((8, 65536, 2048, {}), stream(16, 16)), ((9, 65536, 2048, {}), tile(1)),
+    # more rows of one group: three rounds of 16 x 16, two of 16 x 32, one of 32 x 32
+    ((9, 4096, 4096, {}), stream(16, 16)), ((9, 4112, 4096, {}), stream(16, 32)), ((16, 8192, 4096, {}), stream(16, 32)),
+    ((16, 8224, 4096, {}), stream(16, 16)), ((16, 12288, 4096, {}), stream(16, 16)), ((16, 12304, 4096, {}), stream(16, 32)),
+    ((16, 16384, 4096, {}), stream(16, 32)), ((16, 16416, 4096, {}), tile(4)),
+    ((128, 2048, 4096, {}), stream(32, 32)), ((128, 2080, 4096, {}), tile(4)),
+    ((256, 1024, 4096, {}), stream(32, 32)), ((257, 1024, 4096, {}), tile(4)), ((48, 8192, 4096, {}), tile(4)),
+    # the rows and columns of a streaming workgroup that the tiles cannot take
     ((48, 8192, 4096, dict(skew=1)), stream(64, 32)), ((32, 8192, 4096, dict(skew=1)), stream(32, 32)),
-    ((64, 2048, 4096, {}), stream(16, 32)),
-    # many groups: 2.5 tiles a compute unit with up to 4 rows to a group, 1.25 with more
+    ((37, 4104, 4128, dict(skew=1)), stream(16, 32)),
+    # many groups: 2.5 tiles a compute unit with up to 4 rows to a group, 1.25 with more, a quarter with up to 128
     ((128, 2240, 2048, dict(groups=32)), stream(16, 32)), ((128, 2304, 2048, dict(groups=32)), tile(1)),
     ((160, 1024, 2048, dict(groups=32)), stream(16, 32)), ((160, 1088, 2048, dict(groups=32)), tile(1)),
+    ((512, 256, 2048, dict(groups=8)), stream(16, 32)), ((512, 448, 2048, dict(groups=8)), tile(1)),
+    ((16, 1024, 2048, dict(groups=4)), stream(16, 16)),
     # large tiles from 5/8 of a round, with groups from 3/8 and 160 rows to a group
     ((2560, 4096, 1024, {}), tile(3)), ((2559, 4096, 1024, {}), tile(2)),
     ((1280, 5120, 1024, dict(groups=8)), tile(3)), ((1272, 5120, 1024, dict(groups=8)), tile(2)),
     ((1280, 4864, 1024, dict(groups=8)), tile(2)),
-    # 128 x 128 from 7/8 of a round, with groups from 96 rows to a group
-    ((1024, 3584, 2048, {}), tile(2)), ((1024, 3456, 2048, {}), tile(1)),
+    # 128 x 128 from 13/16 of a round, with GELU from 9/8, and from 96 rows to a group
+    ((1024, 3328, 2048, {}), tile(2)), ((1024, 3200, 2048, {}), tile(1)),
+    ((1024, 4608, 2048, dict(epi=2)), tile(2)), ((1024, 4480, 2048, dict(epi=2)), tile(1)),
     ((1536, 2048, 2048, dict(groups=16)), tile(2)), ((1520, 2048, 2048, dict(groups=16)), tile(1)),
+    ((96, 28672, 2048, {}), tile(2)), ((95, 28672, 2048, {}), tile(1)),
     # a third stage for a long K and up to two tiles a compute unit
     ((1024, 2048, 4096, {}), tile(4)), ((1024, 2112, 4096, {}), tile(1)), ((1024, 2048, 4064, {}), tile(1)),
 ])

@@ -11,12 +11,23 @@ namespace tgemm {
 enum GroupedTile : int { GT_ANY = 0, GT_64 = 1, GT_128 = 2, GT_256 = 3, GT_64_DEEP = 4, GT_ANY_DEEP = 5 };
 
 template <class C>
-__global__ __launch_bounds__(C::NT) void grouped_rows_kernel(GemmParams p, GroupArgs ga) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS_BYTES];
+__device__ __forceinline__ void grouped_rows_tile(GemmParams& p, const GroupArgs& ga, uint8_t* smem) {
   const GroupItem it = group_item(ga, p.M, C::BM, p.tiles_n, workgroup(ga), threadIdx.x & 63);
   if (it.group < 0) return;
   enter_group<C::ES, DTypeInfo<C::CT>::bytes, C::MX>(p, ga, it.group, it.row0, it.rows);
   mfma_tile<C>(p, SkSeg{}, smem, tile_pos(it.local, (it.rows + C::BM - 1) / C::BM, p.tiles_n));
+}
+
+template <class C>
+__global__ __launch_bounds__(C::NT) void grouped_rows_kernel(GemmParams p, GroupArgs ga) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS_BYTES];
+  grouped_rows_tile<C>(p, ga, smem);
+}
+// The same with the registers of two waves a SIMD at most.
+template <class C>
+__global__ __launch_bounds__(C::NT, 2) void grouped_rows_two_kernel(GemmParams p, GroupArgs ga) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS_BYTES];
+  grouped_rows_tile<C>(p, ga, smem);
 }
 
 // 256 x 256 tiles (F) with 128 x 128 ones (Q) where the large would waste the chip:
@@ -176,7 +187,7 @@ __global__ __launch_bounds__(C::NT) void grouped_wgrad_kernel(GemmParams p, Grou
   mfma_tile<C>(p, SkSeg{}, smem, tile_pos(local, p.tiles_m, p.tiles_n));
 }
 
-template <class C>
+template <class C, bool TWO = false>
 hipError_t launch_rows_cfg(GemmParams p, GroupArgs ga, hipStream_t s) {
   p.tiles_n = (p.N + C::BN - 1) / C::BN;
   const int64_t grid = whole_rounds(max_row_tiles(p.M, ga.groups, C::BM) * p.tiles_n);
@@ -188,7 +199,8 @@ hipError_t launch_rows_cfg(GemmParams p, GroupArgs ga, hipStream_t s) {
   }
   return launch_in_slices(grid, C::NT, [&](int64_t first, unsigned n) {
     ga.first = (int)first;
-    hipLaunchKernelGGL((grouped_rows_kernel<C>), dim3(n), dim3(C::NT), 0, s, p, ga);
+    if constexpr (TWO) hipLaunchKernelGGL((grouped_rows_two_kernel<C>), dim3(n), dim3(C::NT), 0, s, p, ga);
+    else hipLaunchKernelGGL((grouped_rows_kernel<C>), dim3(n), dim3(C::NT), 0, s, p, ga);
   });
 }
 
@@ -322,7 +334,7 @@ hipError_t launch_mx_type(const GemmParams& p, const GroupArgs& ga, int tile, in
   switch (tile) {
     case GT_64: return launch_rows_cfg<typename GroupedMxCfg<CT, GT_64>::T>(p, ga, s);
     case GT_64_DEEP: return launch_rows_cfg<typename GroupedMxCfg<CT, GT_64_DEEP>::T>(p, ga, s);
-    case GT_128: return launch_rows_cfg<typename GroupedMxCfg<CT, GT_128>::T>(p, ga, s);
+    case GT_128: return launch_rows_cfg<typename GroupedMxCfg<CT, GT_128>::T, true>(p, ga, s);
     case GT_256: return launch_mixed_cfg<typename Large::T, typename Large::Small>(p, ga, cus, s);
     default: return hipErrorInvalidValue;
   }

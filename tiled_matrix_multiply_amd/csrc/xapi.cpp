@@ -222,33 +222,71 @@ int64_t expected_tiles(const MxArgs& a, int64_t bm, int64_t bn) {
 // Rows of a group that has any, on average.
 int64_t average_rows(const MxArgs& a) { return (a.M + live_groups(a) - 1) / live_groups(a); }
 
-// The kernel of a call (times: one MI355X, constant operands, 256 compute units).
+// Rows and columns of a streaming workgroup (times: one MI355X, constant operands, 256 compute units).
+struct StreamTile {
+  int rows, columns, cost;
+};
+StreamTile stream_tile(const MxArgs& a, int cus) {
+  // Up to 8 rows of one group: the weights' way from memory counts, and more workgroups even out the last
+  // round (1 x 4096 x 4096 4.0 us against 5.2 with 32 columns, 1 x 20480 x 7168 14.3 against 15.7, 1 x 16384 x
+  // 7168, two for each unit exactly, 12.1 against 11.4).
+  if (a.groups == 1 && a.M <= 8 && countable(a, 16, 16)) return {16, 16, 0};
+  if (a.groups == 1) {
+    // More rows of one group: the caches' rate counts, and a compute unit with two workgroups takes almost
+    // twice as long.  A round of each kind (K of 8192: 7.1, 9.4, 12 and 17.6 us; of 2048: 4.1, 4.4, 5.2 and 7.0)
+    // costs about 9, 14, 19 and 30.  37 x 4104 x 4128: 387 of 16 x 32 6.6 us, 258 of 32 x 32 7.2, 129 of 64 x 32
+    // 7.4; 37 x 4096 x 4096: 384, 256 and 128 of them 9.4, 7.7 and 9.0.
+    const StreamTile kinds[] = {{16, 16, 9}, {16, 32, 14}, {32, 32, 19}, {64, 32, 30}};
+    StreamTile best{64, 32, 0x7fffffff};
+    for (const StreamTile& t : kinds) {
+      const int64_t rounds = (expected_tiles(a, t.rows, t.columns) + cus - 1) / cus;
+      if (rounds < 1000 && rounds * t.cost < best.cost && countable(a, t.rows, t.columns))
+        best = {t.rows, t.columns, (int)rounds * t.cost};
+    }
+    return best;
+  }
+  // Groups: as few rows as leave the compute units at most 1.6 workgroups each, up to twice the average, and
+  // half the columns where that is not one each (8 rows in each of 32 groups of 1024 x 4096: 16 x 32 18.8 us, 32 x 32
+  // 17.3, 64 x 32 20.3; 4 in each of 4 of 1024 x 4096: 16 x 16 4.7, 16 x 32 5.6).
+  const int64_t most = 2 * average_rows(a);
+  int rows = 16;
+  while (rows < 64 && ((rows < most && 10 * expected_tiles(a, rows, 32) > 16 * cus) || !countable(a, rows, 32))) rows *= 2;
+  const bool narrow = rows == 16 && countable(a, 16, 16) && expected_tiles(a, 16, 16) <= cus;
+  return {rows, narrow ? 16 : 32, 0};
+}
+
+// The kernel of a call (times as above).
 gemm_grouped_kernel_t pick(const MxArgs& a, int cus) {
   const int64_t rows = average_rows(a), small = expected_tiles(a, 64, 64);
   if (!tiles_fit(a)) return GEMM_GROUPED_STREAM;
   if (stream_fits(a)) {
     // Streaming needs no barrier and starts at once, but reads half lines, and the rows once for every 16 or
-    // 32 columns: it pays where 64 x 64 tiles are few.  One group: 1 x 28672 x 8192 (448 tiles) 24 us against
-    // 28, 16 x 28672 x 8192 37 against 31, 16 x 8192 x 4096 (128) 6.5 against 10.4, 48 rows 10.2 against 10.4.
+    // 32 columns: it pays where 64 x 64 tiles are few.  One group: always up to 8 rows (1 x 28672 x 8192 24 us
+    // against 28); with more, up to three rounds of 16 x 16, two of 16 x 32 or one of 32 x 32 (256 x 1024 x 4096, one
+    // of 32 x 32, 7.6 against 10.3; 320 x 1600 x 8192, one of 64 x 32, 17.9 against 17.3; 16 x 28672 x 8192 37
+    // against 31).
     // Many: 64 rows over 8 groups of 1024 x 1024 (80) 3.7 against 5.2, 32 over 64 of 1024 x 2048 (272) 8.2 against
     // 9.5, 64 over 32 of 2048 x 2048 (544, 2 rows a group) 13.5 against 14.2, 256 rows 16.2 against 14.2, 128 over
-    // 16 of 4096 x 4096 (640) 38 against 30.  Very few: 64 x 4096 x 8192 (64) 14 against 20, 192 x 2048 x 2048 (96)
-    // 7.3 against 6.3.
-    const bool one = a.groups == 1;
-    const int64_t most = (one ? 6 : rows <= 4 ? 10 : 5) * cus;
-    if ((one && a.M <= 8) || (rows <= 32 && 4 * small <= most) || (rows <= 128 && 4 * small <= cus))
+    // 16 of 4096 x 4096 (640) 38 against 30.
+    if (a.groups == 1) {
+      if (stream_tile(a, cus).cost <= 28) return GEMM_GROUPED_STREAM;
+    } else if ((rows <= 32 && 4 * small <= (rows <= 4 ? 10 : 5) * cus) || (rows <= 128 && 4 * small <= cus)) {
       return GEMM_GROUPED_STREAM;
+    }
   }
   // Large tiles, mixed with small ones, from 5/8 of a round on, with uneven groups from 3/8 on if they hold
   // large tiles at all (1536 x 8192 x 1024, 192 of them, 13.5 us against 15.1 on 128 x 128 ones, 2048 x 4096 x
-  // 4096, 128, 33 against 23; 2048 rows over 8 groups of 4096 x 4096, 128, 30 against 36, but 4096 over 32 of
-  // 2048 x 2048, 128, 31 against 24).
+  // 4096, 128, 33 against 23; 4096 rows over 8 uneven groups of 2048 x 2048, 128, 18.1 against 22.9 (even groups
+  // 22.8 against 15.6), but 4096 over 32 of 2048 x 2048, 128, 30 against 27).
   const int64_t large = a.M * ((a.N + 255) / 256);  // in rows of 256
   if (a.groups == 1 ? 8 * large >= 5 * 256 * cus : rows >= 160 && 8 * large >= 3 * 256 * cus) return GEMM_GROUPED_MFMA_256;
-  // 128 x 128 from most of a round on (1024 x 4096 x 4096, 256 of them, 17.2 us against 20.8 on 64 x 64 ones,
-  // 1024 x 2048 x 2048, 128, 10.4 against 8.2), and with groups that fill them (64 rows a group 24.5 against
-  // 19.2, 96 rows 24.2 against 24.3, 128 rows 24.1 against 26.3: 32 groups of 2048 x 2048).
-  if (8 * expected_tiles(a, 128, 128) >= 7 * cus && (a.groups == 1 || rows >= 96)) return GEMM_GROUPED_MFMA_128;
+  // 128 x 128 from 13/16 of a round on (1024 x 3456 x 2048, 216 of them, 10.7 us against 11.6 on 64 x 64 ones, 2048 x
+  // 1536 x 2048, 192, 10.7 against 10.0), with GELU, which takes longest where one round has a few waves only, from
+  // 9/8 (1024 x 4096 x 2048, 256, 15.0 against 13.4, 2048 x 2560 x 2048, 320, 17.9 against 19.7), and with rows
+  // that fill them (64 rows a group 23.5 against 19.0, 128 rows 26.8 against 28.7: 32 uneven groups of 2048 x 2048;
+  // 32 x 28672 x 4096 17.8 against 14.5).
+  const int least = a.epi & GEMM_EPI_GELU ? 18 : 13;
+  if (rows >= 96 && 16 * expected_tiles(a, 128, 128) >= least * cus) return GEMM_GROUPED_MFMA_128;
   return GEMM_GROUPED_MFMA_64;
 }
 
@@ -285,21 +323,10 @@ gemm_status_t run(gemm_handle_t h, gemm_grouped_kernel_t kernel, void* stream, c
   const hipStream_t s = static_cast<hipStream_t>(stream);
   tgemm::DeviceGuard g(h->device);
   if (kernel == GEMM_GROUPED_STREAM) {
-    // A workgroup has as few rows as leave the compute units at most 1.6 workgroups each (48 x 8192 x 4096 with
-    // 16 rows, 768 of them, 13.0 us, with 32 12.4, with 64 10.2; 37 x 4104 x 4128, 387, 6.6, 7.2 and 7.4), and half
-    // the columns where that is not one each (1 x 4096 x 4096 4.0 against 5.2, 16 x 8192 x 4096, two each, 7.4 against
-    // 6.5) or rows weigh little: twice as many workgroups even out the last round (1 x 20480 x 7168 14.3 against
-    // 15.7, 1 x 16384 x 7168, two each exactly, 12.1 against 11.4).
-    // (No more than there are: a group of several may have twice the average.)
-    const int64_t most = a.groups == 1 ? a.M : 2 * average_rows(a);
-    int rows = 16;
-    while (rows < 64 && rows < most && 10 * expected_tiles(a, rows, 32) > 16 * h->cu_count) rows *= 2;
-    while (rows < 64 && !countable(a, rows, 32)) rows *= 2;
-    const bool narrow = rows == 16 && countable(a, 16, 16) &&
-                        ((a.groups == 1 && a.M <= 8) || expected_tiles(a, 16, 16) <= h->cu_count);
+    const StreamTile t = stream_tile(a, h->cu_count);
     p.ldsa = step(a.ldsa, a.M, 0);
     p.ldsb = step(a.ldsb, a.N, 0);
-    return status(tgemm::launch_stream_mx(p, ga, a.ct, rows, narrow ? 16 : 32, s));
+    return status(tgemm::launch_stream_mx(p, ga, a.ct, t.rows, t.columns, s));
   }
   const bool deep = a.K >= 4096 && expected_tiles(a, 64, 64) <= 2 * h->cu_count;  // three stages (GroupedMxCfg)
   const int tile = kernel == GEMM_GROUPED_MFMA_64 ? (deep ? 4 : 1) : kernel == GEMM_GROUPED_MFMA_128 ? 2 : 3;
