@@ -270,6 +270,21 @@ def test_route_close_keys(g):
     check_route(g, big, 8, "bf16", kind="sigmoid", bias=bias)
 
 
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_route_many_experts(g, kind):
+    """More than 256 experts, eight to a lane, around the borders of the tokens to a workgroup."""
+    for i, n in enumerate([3, 66, 256, 257, 400, 512, 513]):
+        for j, (E, groups, best, k) in enumerate([(300, 1, 1, 4), (512, 1, 1, 8), (512, 8, 3, 8), (416, 4, 2, 32), (513, 1, 1, 6)]):
+            print(f"[route] many {kind} {n} {E} {groups} {k}", flush=True)
+            x = logits(n, E, i + j)
+            x[n // 2] = -INF
+            x[n - 1, 7:] = -INF
+            x[0] = np.float32(0.5) + np.float32(1e-6) * RNG([i, j]).integers(-2, 3, E)     # close and equal keys
+            x = x.astype(np.float32).astype(np.float64)
+            bias = 0.2 * RNG([i, j]).standard_normal(E) if (i + j) % 2 else None
+            check_route(g, x, k, "f32", kind=kind, bias=bias, groups=groups, best=best, of=1 + j % 2, renorm=i % 2 == 0)
+
+
 def test_route_no_tokens_and_many(g):
     import torch
     _, _, _, offsets = call_route(g, np.zeros((0, 5)), 2)[0]

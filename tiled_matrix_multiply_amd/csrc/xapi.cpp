@@ -56,7 +56,7 @@ gemm_status_t check_sizes(int64_t T, int64_t E, int64_t top, gemm_dtype_t xt, in
   return GEMM_OK;
 }
 
-int64_t route_bytes(int64_t T, int64_t E) { return T <= 64 ? 0 : tgemm::route_blocks(T) * tgemm::route_row_bytes(E); }
+int64_t route_bytes(int64_t T, int64_t E) { return T <= 64 ? 0 : tgemm::route_blocks(T, E) * tgemm::route_row_bytes(E); }
 
 gemm_status_t check_route(int64_t T, int64_t E, int64_t top, const void* x, int64_t ldl, gemm_dtype_t xt, int score,
                           const float* bias, int64_t groups, int64_t top_groups, int group_top, int renorm,
