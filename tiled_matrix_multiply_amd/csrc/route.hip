@@ -933,9 +933,10 @@ hipError_t launch_route(const RouteArgs& args, hipStream_t s) {
   p.run_size = p.E / p.groups;
   p.per_top = (65536 + p.top - 1) / p.top;
   const int TB = route_block_tokens(p.T, p.E);
-  // Lanes of a token: 16 hold a choice of at most 16; a few tokens are over sooner with 64 lanes each, and
-  // so many experts do not fit 16.  Experts of a lane: the fewest that hold all of them, runs of them in
-  // lanes of their own (2000 x 512 with 16 to a lane 24.0 us, with 8 17.7).
+  // Lanes of a token: 16 hold a choice of at most 16 from at most 256 experts; up to 8 tokens of more than 128
+  // are over sooner with 64 (4 x 256: 6.5 us against 7.0, 16 x 256 8.8 against 7.3; 4 x 128 6.8 against 6.1).
+  // Experts of a lane: the fewest that hold all of them, runs of them in lanes of their own (2000 x 512
+  // with 16 to a lane 24.0 us, with 8 17.7).
   auto fits = [&](int L, int V) {
     if (p.groups == 1) {
       p.run_lanes = 6;
@@ -947,7 +948,7 @@ hipError_t launch_route(const RouteArgs& args, hipStream_t s) {
     return p.groups << p.run_lanes <= L;
   };
   hipError_t e;
-  if (p.top > 16 || p.T <= 16 || !fits(16, 16))
+  if (p.top > 16 || !fits(16, 16) || (p.T <= 8 && !fits(16, 8)))
     e = fits(64, 1)    ? route_launch<64, 1, 1024>(p, TB, s)
         : fits(64, 4)  ? route_launch<64, 4, 1024>(p, TB, s)
         : fits(64, 8)  ? route_launch<64, 8, 1024>(p, TB, s)
