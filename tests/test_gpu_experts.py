@@ -938,12 +938,12 @@ def test_mx_refuses_what_a_kernel_cannot(g):
     C = torch.zeros(16, 16, device="cuda:0", dtype=torch.bfloat16)
     for kernel, shift in ((1, 0), (2, 1), (3, 1), (4, 1), (6, 0), (-1, 0)):
         with pytest.raises(tmm.GemmError):
-            g.run_grouped_mx(z[shift:], z[1024:], z[2048:], z[3072:], C, None, groups=1, M=16, N=16, K=64, ldsa=16,
+            g.run_grouped_mx(z[shift:], z[768:], z[1536:], z[2304:], C, None, groups=1, M=16, N=16, K=64, ldsa=16,
                              ldsb=16, kernel=kernel)
     # scale rows that are no multiple of 16 bytes: tiles refuse, AUTO streams
     with pytest.raises(tmm.GemmError):
-        g.run_grouped_mx(z, z[1024:], z[2048:], z[3072:], C, None, groups=1, M=16, N=16, K=64, kernel=2)
-    g.run_grouped_mx(z, z[1024:], z[2048:], z[3072:], C, None, groups=1, M=16, N=16, K=64)
+        g.run_grouped_mx(z, z[768:], z[1536:], z[2304:], C, None, groups=1, M=16, N=16, K=64, kernel=2)
+    g.run_grouped_mx(z, z[768:], z[1536:], z[2304:], C, None, groups=1, M=16, N=16, K=64)
 
 
 # ---------------------------------------------------------------------------- together --
