@@ -256,6 +256,31 @@ def test_route_nan_and_infinity_are_not_silent(g):
             assert np.isfinite(weight[4:]).all()
 
 
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_route_nan_in_masked_places(g, kind):
+    """An expert that a bias of -infinity takes out stays out whatever its logit: NaN, infinity; in a
+    softmax these make every score NaN, and the experts that are left come in their order."""
+    for E, groups, best in ((32, 1, 1), (32, 4, 2), (200, 1, 1), (300, 1, 1)):
+        for n in (3, 20):
+            x = logits(n, E, E)
+            x[0, 5] = NAN
+            x[1, 5], x[1, 9] = INF, NAN
+            x[2, 9] = NAN
+            bias = 0.1 * RNG(E).standard_normal(E)
+            bias[5] = bias[9] = -INF
+            for renorm in (False, True):
+                (expert, weight, place, _), _ = call_route(g, x, 4, "f32", kind=kind, bias=bias, groups=groups, best=best,
+                                                           renorm=renorm)
+                assert not np.isin(expert, [5, 9]).any() and (expert >= 0).all() and (place >= 0).all(), (E, groups, n)
+                if kind == "sigmoid":
+                    ref = reference(np.where(np.isin(np.arange(E), [5, 9]), -INF, x.astype(np.float32).astype(np.float64)), 4,
+                                    kind, bias.astype(np.float32).astype(np.float64), groups, best, 1, renorm, 1.0)
+                    assert np.array_equal(expert, ref[0]) and np.isfinite(weight).all()
+                else:
+                    first = [e for e in range(E) if e not in (5, 9)][:4]
+                    assert all(expert[t].tolist() == first for t in range(3))
+
+
 def test_route_close_keys(g):
     """Keys that fp32 cannot tell apart are ordered as 64 bits order them."""
     E, n = 128, 400

@@ -423,7 +423,7 @@ __device__ __forceinline__ bool choose_quick(const RouteArgs& p, const Layout& l
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const float k = fminf(s[i] + bias[i], inf);  // a NaN as infinity
-      key[i] = x[i] == kNone ? kNone : k;
+      key[i] = x[i] == kNone || bias[i] == kNone ? kNone : k;
     }
   } else {
 #pragma unroll
