@@ -7,6 +7,10 @@
 // of a fragment holds row (column) l % 16 and the 32 elements k = 32 (l / 16) .. + 31 of a step of 128, 16
 // bytes, with the one scale that belongs to them.  A unit is U steps; its 4 U scale bytes of a row come
 // in one load, the same for the four lanes of the row, and each lane moves its own byte of a step down.
+//
+// Up to 8 rows the weights' bytes bound it (1 x 28672 x 8192 24.8 us, 5.0 TB/s; 32 rows over 64 groups of 1024 x
+// 2048 9.2, 28 MB), with more the caches' rate: every tile reads its rows and columns again (48 x 4096 x 8192, 256
+// tiles of 32 x 32, 12.2 us, 67 MB).
 #include <type_traits>
 
 #include "grouped.hpp"

@@ -16,6 +16,11 @@
 // number of bits below its own.  Up to 64 tokens are one workgroup and one launch.  More leave a
 // table of blocks x experts counts (a byte each, at most 64), from which a second kernel takes where
 // each block's rows start.
+//
+// What bounds it are chains of dependent steps, not the bytes: the logits' way from memory, `top` maxima across
+// lanes, the counts' way through memory to the second kernel.  One token of 256 experts (sigmoid, bias, 4 of 8
+// groups) 6.9 us, 8191 tokens 18 (13.2 and 7.1 by themselves; 8.4 MB, 2 us at the rate of a copy), 16384 of 128
+// (softmax) 14.7.
 #include "experts.hpp"
 #include "grouped.hpp"
 
@@ -821,6 +826,8 @@ __global__ __launch_bounds__(256) void route_place_kernel(RouteArgs p, int TB, i
 //   dx_e = s_e (g_e - sum_j g_j s_j) = s_e (g_e U + sum_j s_j (g_e - g_j)),   U = the sum of the others' s
 // (g_e = 0 for what was not chosen).  Written as differences none of them cancels where one weight is
 // near 1.
+// Its bytes bound it where there are many tokens: 16384 x 128 in fp32 6.4 us, 16384 x 512 10.4 (6.5 TB/s, out of
+// the memory-side cache).
 // A token's row of results lies in LDS between what every expert gets and what the chosen get; only the
 // wave that owns it touches it, so its writes and reads keep their order without a barrier.
 __device__ __forceinline__ void row_written() {
