@@ -725,11 +725,18 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs p, int TB) {
 // The second kernel: places within a block become places in the whole.  Every workgroup adds up the
 // table of counts, all blocks' and those before its own (the table is read from the L2), 4 experts to a
 // thread: bytes apart in sums of 16 bits, flushed before they could pass 65535 (1000 rows of at most 64).
-__global__ __launch_bounds__(256) void route_place_kernel(RouteArgs p, int TB, int blocks) {
+// It is a chain of waits (of 5.4 us by itself a launch is 2): the loads of a thread go out together, one pass
+// gives both sums, nothing is divided but by powers of two (cols: threads to a row of the table), and long
+// tables have 1024 threads (256 rows of 256 bytes: FIGP).
+__global__ __launch_bounds__(1024) void route_place_kernel(RouteArgs p, int TB, int blocks, int cols) {
   __shared__ int total[1024], before[1024], start[1024];
-  __shared__ int part[4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int b0 = (int)((int64_t)blockIdx.x * blocks / gridDim.x), b1 = (int)((int64_t)(blockIdx.x + 1) * blocks / gridDim.x);
+  __shared__ int part[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, threads = blockDim.x;
+  int b0 = blockIdx.x, b1 = b0 + 1;
+  if ((int)gridDim.x < blocks) {  // (256 of them at most, and less than 2^23 blocks)
+    b0 = (int)(blockIdx.x * (uint32_t)blocks / gridDim.x);
+    b1 = (int)((blockIdx.x + 1) * (uint32_t)blocks / gridDim.x);
+  }
   // the first block's pairs, fetched while the table is
   constexpr int AHEAD = 2;
   const int64_t at0 = (int64_t)b0 * TB * p.top;
@@ -737,54 +744,56 @@ __global__ __launch_bounds__(256) void route_place_kernel(RouteArgs p, int TB, i
   int e_first[AHEAD], rank_first[AHEAD];
 #pragma unroll
   for (int q = 0; q < AHEAD; ++q) {
-    const int i = min(tid + 256 * q, pairs0 - 1);
+    const int i = min(tid + threads * q, pairs0 - 1);
     e_first[q] = p.expert[at0 + i];
     rank_first[q] = p.place[at0 + i];
   }
-  for (int e = tid; e < 1024; e += 256) total[e] = before[e] = 0;
+  const int row = (int)route_row_bytes(p.E), lc = __builtin_ctz(cols), rows = threads >> lc;
+  const int c = min(tid & (cols - 1), row / 4 - 1), r = tid >> lc;
+  for (int e = tid; e < row; e += threads) total[e] = before[e] = 0;
   __syncthreads();
-  const int64_t row = route_row_bytes(p.E);
-  const int per = (int)(row / 4), rows = 256 / per, c = tid % per, r = tid / per;
-  if (r < rows) {
-    const uint8_t* const table = p.ws + 4 * c;
-    auto add_up = [&](int from, int to, int* sums, int* more) {  // blocks from, from + rows, .. below to
-      for (int chunk = from; chunk < to; chunk += 1000 * rows) {
-        const int end = (int)min((int64_t)to, (int64_t)chunk + 1000 * rows);
-        uint32_t even = 0, odd = 0;
-        for (int b = chunk; b < end; b += 16 * rows) {
-          uint32_t v[16];
+  for (int chunk = 0; chunk < blocks; chunk += 1000 * rows) {
+    const int here = min(1000 * rows, blocks - chunk);  // rows of the table
+    const uint8_t* const table = p.ws + (int64_t)chunk * row;
+    uint32_t even = 0, odd = 0, even_b = 0, odd_b = 0;
+    auto batch = [&](int b, auto count) {  // rows b + q * rows of the chunk
+      constexpr int N = decltype(count)::value;
+      uint32_t v[N];
 #pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            const int64_t at = min(b + (int64_t)q * rows, (int64_t)end - 1);
-            v[q] = *reinterpret_cast<const uint32_t*>(table + at * row);
-          }
+      for (int q = 0; q < N; ++q)
+        v[q] = *reinterpret_cast<const uint32_t*>(table + (uint32_t)(min(b + q * rows, here - 1) * row + 4 * c));
 #pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            const uint32_t w = b + (int64_t)q * rows < end ? v[q] : 0u;
-            even += w & 0x00ff00ffu;
-            odd += (w >> 8) & 0x00ff00ffu;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = (int)(((i & 1 ? odd : even) >> (8 * (i & 2))) & 0xffffu);
-          atomicAdd(&sums[4 * c + i], n);
-          if (more) atomicAdd(&more[4 * c + i], n);
-        }
+      for (int q = 0; q < N; ++q) {
+        const int at = b + q * rows;
+        const uint32_t w = at < here ? v[q] : 0u, e = w & 0x00ff00ffu, o = (w >> 8) & 0x00ff00ffu;
+        even += e;
+        odd += o;
+        even_b += chunk + at < b0 ? e : 0u;
+        odd_b += chunk + at < b0 ? o : 0u;
       }
     };
-    add_up(r, b0, total, before);
-    add_up(b0 + ((r - b0) % rows + rows) % rows, blocks, total, nullptr);
+    if (here <= 4 * rows) {
+      batch(r, std::integral_constant<int, 4>{});
+    } else {
+      for (int b = r; b - r < here; b += 16 * rows) batch(b, std::integral_constant<int, 16>{});
+    }
+    if ((tid & (cols - 1)) < row / 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        atomicAdd(&total[4 * c + i], (int)(((i & 1 ? odd : even) >> (8 * (i & 2))) & 0xffffu));
+        if (b0 > 0) atomicAdd(&before[4 * c + i], (int)(((i & 1 ? odd_b : even_b) >> (8 * (i & 2))) & 0xffffu));
+      }
+    }
   }
   __syncthreads();
   int carry = 0;
-  for (int base = 0; base < p.E; base += 256) {
+  for (int base = 0; base < p.E; base += threads) {
     const int e = base + tid;
     const int own = e < p.E ? total[e] : 0, v = scan_add(own);
     if (lane == 63) part[wave] = v;
     __syncthreads();
     int b = carry, all = 0;
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < threads / 64; ++w) {
       if (w < wave) b += part[w];
       all += part[w];
     }
@@ -803,17 +812,17 @@ __global__ __launch_bounds__(256) void route_place_kernel(RouteArgs p, int TB, i
     if (b == b0) {
 #pragma unroll
       for (int q = 0; q < AHEAD; ++q)
-        if (tid + 256 * q < n && e_first[q] >= 0) p.place[at0 + tid + 256 * q] = rank_first[q] + start[e_first[q]];
-      done = 256 * AHEAD;
+        if (tid + threads * q < n && e_first[q] >= 0) p.place[at0 + tid + threads * q] = rank_first[q] + start[e_first[q]];
+      done = threads * AHEAD;
     }
-    for (int i = done + tid; i < n; i += 256) {
+    for (int i = done + tid; i < n; i += threads) {
       const int64_t at = t0 * p.top + i;
       const int e = p.expert[at];
       if (e >= 0) p.place[at] += start[e];
     }
     if (b + 1 == b1) break;
     __syncthreads();
-    for (int e = tid; e < p.E; e += 256) start[e] += p.ws[b * row + e];
+    for (int e = tid; e < p.E; e += threads) start[e] += p.ws[(int64_t)b * row + e];
     __syncthreads();
   }
 }
@@ -969,7 +978,10 @@ hipError_t launch_route(const RouteArgs& args, hipStream_t s) {
   const bool one = p.T <= 64;
   if (e != hipSuccess || one) return e;
   const int64_t blocks = route_blocks(p.T, p.E);
-  hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)(blocks < 256 ? blocks : 256)), dim3(256), 0, s, p, TB, (int)blocks);
+  int cols = 4;  // threads of a row of the table
+  while (4 * cols < route_row_bytes(p.E)) cols *= 2;
+  const int threads = blocks * cols > 16 * 256 ? 1024 : 256;
+  hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)(blocks < 256 ? blocks : 256)), dim3(threads), 0, s, p, TB, (int)blocks, cols);
   return hipGetLastError();
 }
 
