@@ -34,8 +34,8 @@ typedef enum gemm_score {
   GEMM_SCORE_SIGMOID = 1
 } gemm_score_t;
 
-/* Workspace bytes gemm_route needs: 0 for up to 64 tokens.  A negative status for sizes that gemm_route
- * refuses.  Touches no device. */
+/* Workspace bytes gemm_route needs: 0 for up to 64 tokens of up to 128 experts (32 of up to 256, 16 of
+ * more).  A negative status for sizes that gemm_route refuses.  Touches no device. */
 GEMM_API int64_t gemm_route_workspace_bytes(int64_t tokens, int64_t experts);
 
 /* The experts of each token and the order of the rows that go to them.

@@ -725,7 +725,7 @@ def quantize_rows(handle, X, Q, scales, *, M, K, x_type="bf16", ldx=None, ldq=No
 
 
 def route_workspace_bytes(tokens: int, experts: int) -> int:
-    """Bytes of the workspace that `route` needs (0 for up to 64 tokens).  Raises GemmError for sizes it
+    """Bytes of the workspace that `route` needs (0 for a few tokens).  Raises GemmError for sizes it
     refuses."""
     n = gemm_route_workspace_bytes(tokens, experts)
     if n < 0:

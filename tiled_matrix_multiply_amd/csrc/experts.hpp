@@ -37,13 +37,17 @@ struct RouteGradArgs {
   int64_t ldd;
 };
 
-// Tokens of one workgroup of the router, at most 64: a token is a bit of a 64-bit mask there.  Few to a
-// workgroup where there are few, so that they have more compute units; more where there are more, for every
-// workgroup of the second kernel reads all workgroups' counts.  Past 256 experts a token has a wave of its own
-// (202 tokens of 416 experts: 13.0 us with 4, 14.6 with 16; 1000 of 300: 17.1 and 16.5).
+// Tokens that one workgroup of the router takes alone, in one launch: as many as it can hold at a time (64 of
+// 256 experts would be two rounds: 12.6 us against 10.0 for 65 in two launches; 64 of 512 four: 24.5 against 10.5).
+inline int route_alone(int64_t E) { return E <= 128 ? 64 : E <= 256 ? 32 : 16; }
+// Tokens of a workgroup, at most 64: a token is a bit of a 64-bit mask there.  Few where there are few tokens, so
+// that they have more compute units; more where there are more, for every workgroup of the second kernel reads
+// all workgroups' counts.  Past 256 experts a token has a wave of its own (202 tokens of 416 experts: 13.0 us with
+// 4, 14.6 with 16; 1000 of 300: 17.1 and 16.5).
 inline int route_block_tokens(int64_t T, int64_t E) {
-  if (E > 256 && T > 64 && T <= 512) return T <= 256 ? 4 : 8;
-  return T <= 64 ? 64 : T <= 4096 ? 16 : T <= 8192 ? 32 : 64;
+  if (T <= route_alone(E)) return 64;
+  if (E > 256 && T <= 512) return T <= 256 ? 4 : 8;
+  return T <= 4096 ? 16 : T <= 8192 ? 32 : 64;
 }
 inline int64_t route_blocks(int64_t T, int64_t E) { return (T + route_block_tokens(T, E) - 1) / route_block_tokens(T, E); }
 constexpr __host__ __device__ int64_t route_row_bytes(int64_t E) { return (E + 15) / 16 * 16; }

@@ -13,7 +13,7 @@
 //
 // The order of the rows needs no sorting: within a workgroup of up to 64 tokens each expert has a mask
 // with a bit for each token (set in any order, the same in the end), and a pair's rank there is the
-// number of bits below its own.  Up to 64 tokens are one workgroup and one launch.  More leave a
+// number of bits below its own.  Some tokens (route_alone) are one workgroup and one launch.  More leave a
 // table of blocks x experts counts (a byte each, at most 64), from which a second kernel takes where
 // each block's rows start.
 //
@@ -466,9 +466,11 @@ __device__ __forceinline__ bool choose_quick(const RouteArgs& p, const Layout& l
     const uint32_t head = u[0] & ~LOW, best = max_across<L>(head);
     const bool own = sub == first_lane<L>(head == best, lane);
     if (own) record[j] = u2_t{best, (uint32_t)(sub * V) + LOW - (u[0] & LOW)};
-    // (selects: moves inside the branch cost the loop twice as many instructions)
+    // (a mask that the compiler cannot see through: it would make a branch of the selects, with twice the moves)
+    uint32_t all = own ? ~0u : 0u;
+    asm volatile("" : "+v"(all));
 #pragma unroll
-    for (int i = 0; i < V; ++i) u[i] = own ? (i + 1 < V ? u[i + 1 < V ? i + 1 : i] : 0u) : u[i];
+    for (int i = 0; i < V; ++i) u[i] = (all & (i + 1 < V ? u[i + 1 < V ? i + 1 : i] : 0u)) | (~all & u[i]);
     return best;
   };
   auto apart = [&](uint32_t a, uint32_t b) {  // a >= b, without their last bits
@@ -725,9 +727,9 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs p, int TB) {
 // The second kernel: places within a block become places in the whole.  Every workgroup adds up the
 // table of counts, all blocks' and those before its own (the table is read from the L2), 4 experts to a
 // thread: bytes apart in sums of 16 bits, flushed before they could pass 65535 (1000 rows of at most 64).
-// It is a chain of waits (of 5.4 us by itself a launch is 2): the loads of a thread go out together, one pass
-// gives both sums, nothing is divided but by powers of two (cols: threads to a row of the table), and long
-// tables have 1024 threads (256 rows of 256 bytes: FIGP).
+// It is a chain of waits: the loads of a thread go out together, one pass gives both sums, nothing is divided
+// but by powers of two (cols: threads to a row of the table), and long tables have 1024 threads (63 rows of 64
+// bytes 3.4 us, 256 of 256 5.1; with divisions, two passes and 256 threads 5.4 and 7.1).
 __global__ __launch_bounds__(1024) void route_place_kernel(RouteArgs p, int TB, int blocks, int cols) {
   __shared__ int total[1024], before[1024], start[1024];
   __shared__ int part[16];
@@ -975,7 +977,7 @@ hipError_t launch_route(const RouteArgs& args, hipStream_t s) {
         : fits(16, 4) ? route_launch<16, 4, 1024>(p, TB, s)
         : fits(16, 8) ? route_launch<16, 8, 1024>(p, TB, s)
                       : (fits(16, 16), route_launch<16, 16, 512>(p, TB, s));
-  const bool one = p.T <= 64;
+  const bool one = p.T <= route_alone(p.E);
   if (e != hipSuccess || one) return e;
   const int64_t blocks = route_blocks(p.T, p.E);
   int cols = 4;  // threads of a row of the table

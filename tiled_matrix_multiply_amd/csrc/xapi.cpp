@@ -56,7 +56,9 @@ gemm_status_t check_sizes(int64_t T, int64_t E, int64_t top, gemm_dtype_t xt, in
   return GEMM_OK;
 }
 
-int64_t route_bytes(int64_t T, int64_t E) { return T <= 64 ? 0 : tgemm::route_blocks(T, E) * tgemm::route_row_bytes(E); }
+int64_t route_bytes(int64_t T, int64_t E) {
+  return T <= tgemm::route_alone(E) ? 0 : tgemm::route_blocks(T, E) * tgemm::route_row_bytes(E);
+}
 
 gemm_status_t check_route(int64_t T, int64_t E, int64_t top, const void* x, int64_t ldl, gemm_dtype_t xt, int score,
                           const float* bias, int64_t groups, int64_t top_groups, int group_top, int renorm,
@@ -364,7 +366,7 @@ gemm_status_t gemm_route(gemm_handle_t h, void* stream, int64_t tokens, int64_t 
   if (st != GEMM_OK) return st;
   const tgemm::RouteArgs p{logits, ldl, (int)tokens, (int)experts, (int)top, (int)x_type, (int)score, bias, (int)groups,
                            (int)top_groups, group_top, renorm, scale, expert, weight, place, offsets,
-                           tokens <= 64 ? nullptr : static_cast<uint8_t*>(workspace), 0, 0, 0};
+                           tokens <= tgemm::route_alone(experts) ? nullptr : static_cast<uint8_t*>(workspace), 0, 0, 0};
   tgemm::DeviceGuard g(h->device);
   return status(tgemm::launch_route(p, static_cast<hipStream_t>(stream)));
 }
