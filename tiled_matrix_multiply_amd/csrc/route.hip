@@ -19,8 +19,8 @@
 //
 // What bounds it are chains of dependent steps, not the bytes: the logits' way from memory, `top` maxima across
 // lanes, the counts' way through memory to the second kernel.  One token of 256 experts (sigmoid, bias, 4 of 8
-// groups) 6.9 us, 8191 tokens 18 (13.2 and 7.1 by themselves; 8.4 MB, 2 us at the rate of a copy), 16384 of 128
-// (softmax) 14.7.
+// groups) 7.0 us, 8191 tokens 17 to 19 (14 and 5.2 by themselves; 8.4 MB, 2 us at the rate of a copy), 16384 of
+// 128 (softmax) 14.0.
 #include "experts.hpp"
 #include "grouped.hpp"
 
