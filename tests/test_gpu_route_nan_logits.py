@@ -1,0 +1,38 @@
+"""A NaN logit in the router where the experts of a lane are all NaN: the choice is that of the definition (a
+key that is NaN counts as +infinity), for every place of the NaN, with keys below 0.
+
+Choices, places and offsets have to be equal; the weights' bounds are test_gpu_experts.py's."""
+import numpy as np
+import pytest
+
+from test_gpu_experts import INF, NAN, RNG, check_route, g, logits  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# (experts, the run of neighbours that are NaN: as many as a lane holds)
+@pytest.mark.parametrize("E,run", [(2, 1), (8, 1), (16, 1), (64, 4), (60, 4), (128, 8), (256, 16), (256, 4), (512, 8), (1024, 16)])
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+def test_route_nan_at_each_expert(g, kind, E, run):  # noqa: F811
+    """Every aligned run of a lane's experts in turn, with a bias that makes the other keys negative.  The same
+    tokens alone and in a batch: a few tokens have other lanes than many."""
+    x = logits(E // run + 5, E, run)
+    for i in range(E // run):
+        x[i, i * run:(i + 1) * run] = NAN
+    x[-1], x[-2], x[-3] = NAN, -INF, np.where(np.arange(E) % 3 == 0, NAN, -INF)
+    x[-4, ::2] = NAN
+    x = x[RNG(E).permutation(len(x))]
+    bias = -2 + 0.1 * RNG([E, run]).standard_normal(E)
+    for k in sorted({1, 2, 4, 8, 16, min(E, 20)}):
+        if k > E:
+            continue
+        print(f"[route] NaN {kind} {E} {run} {k}", flush=True)
+        for renorm in (False, True) if kind == "sigmoid" else (False,):
+            check_route(g, x, k, "f32", kind=kind, bias=bias, renorm=renorm)
+        check_route(g, x[:5], k, "bf16", kind=kind, bias=bias)
+        check_route(g, np.concatenate([x] * (1 + 70 // len(x))), k, "f16", kind=kind, bias=bias)
+        check_route(g, x, k, "f32", kind=kind)
+    for groups, best in ((2, 1), (4, 2)):
+        if E % groups == 0:
+            for of in (1, 2):
+                check_route(g, x, min(4, best * E // groups), "f32", kind=kind, bias=bias, groups=groups, best=best, of=of)

@@ -532,12 +532,15 @@ __device__ __forceinline__ bool choose_quick(const RouteArgs& p, const Layout& l
 }
 
 // The scores' common parts over a token: the largest logit and, for softmax, the sum of exp(x - largest).
+// NaN is left out of the maximum on either side of each step, so that all lanes of the token get the same (a
+// comparison would leave it out on one side only, and the bound on the keys' errors and the number of
+// candidates, which go by this, would differ from lane to lane).
 template <int L, int V>
 __device__ __forceinline__ float largest(const float (&x)[V]) {
   float m = x[0];
 #pragma unroll
   for (int i = 1; i < V; ++i) m = fmaxf(m, x[i]);
-  return max_across<L>(m);
+  return across<L>(m, [](float a, float b) { return fmaxf(a, b); });
 }
 template <int L, int V, class S>
 __device__ __forceinline__ S softmax_sum(const float (&x)[V], float x_max) {
