@@ -481,17 +481,20 @@ __device__ __forceinline__ bool choose_quick(const RouteArgs& p, const Layout& l
   };
   uint32_t last = 0;
   for (int j = 0; j < p.top; ++j) last = next(j);
-  // Those that were not chosen but may be worth as much as the last one come behind it, up to four.
+  // Those that were not chosen but may be worth as much as the last one come behind it, up to four and up to
+  // the token's lanes: ranked below, no more than that, or one of them would get the place of another token's
+  // first (where there are more, the token is chosen again).
   int found = p.top;
   if (last >= FINITE) {
     const int most = p.top + 4 < L ? p.top + 4 : L;
     for (;;) {
       const uint32_t r = next(found);
       if (r < FINITE || apart(last, r)) break;
-      if (++found > most) {
+      if (found == most) {
         sure = false;
         break;
       }
+      ++found;
     }
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
