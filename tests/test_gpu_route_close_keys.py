@@ -63,3 +63,19 @@ def test_route_near_biased_keys(g, kind, E):  # noqa: F811
             if E % 4 == 0:
                 check_route(g, x, k, "f32", kind=kind, bias=1e-7 * rng.standard_normal(E), groups=4, best=3, of=2)
                 check_route(g, x, k, "f32", kind=kind, groups=4, best=3, of=2)
+
+
+def test_route_scores_below_the_normal_numbers(g):  # noqa: F811
+    """Sigmoid scores under 2^-126 with biases of their size: the sums are compared as 64 bits have them."""
+    rng = RNG(7)
+    for E, k in ((8, 3), (16, 16), (60, 6), (256, 16), (600, 20)):
+        for n in (3, 40, 150):
+            x = -(86 + 4 * rng.random((n, E)))
+            x[0] = -100 - rng.random(E)
+            x[1] = -700 - 10 * rng.random(E)
+            bias = (4e-39 * rng.random(E)).astype(np.float32).astype(np.float64)
+            print(f"[route] tiny {E} {k} {n}", flush=True)
+            check_route(g, x, k, "f32", kind="sigmoid", bias=bias)
+            check_route(g, x, k, "f32", kind="sigmoid", bias=np.zeros(E))
+            if E % 4 == 0:
+                check_route(g, x, min(k, 3 * E // 4), "f32", kind="sigmoid", bias=bias, groups=4, best=3, of=2)

@@ -413,8 +413,9 @@ __device__ __forceinline__ bool choose_quick(const RouteArgs& p, const Layout& l
     // Relative errors: the exponential's argument is off by half a step or two of itself, the function
     // and the reciprocal by a step.  z exp(-z) <= 0.37, and z s(-z) falls from z = 1.3 on, so that the
     // argument's part is largest at the largest score.  softmax: its sum is off by up to 10 half steps.
+    // Absolute: a sigmoid below 2^-126 is 0 here, and a softmax's bound is far above that.
     if (p.score) {
-      slack = __builtin_amdgcn_rcpf(1.0f + quick_exp(-x_max)) * (0x1p-21f + fmaxf(1.3f, -x_max) * 0x1p-22f);
+      slack = __builtin_amdgcn_rcpf(1.0f + quick_exp(-x_max)) * (0x1p-21f + fmaxf(1.3f, -x_max) * 0x1p-22f) + 0x1p-125f;
 #pragma unroll
       for (int i = 0; i < V; ++i) s[i] = __builtin_amdgcn_rcpf(1.0f + quick_exp(-x[i]));
     } else {
