@@ -59,7 +59,8 @@ GEMM_API int64_t gemm_route_workspace_bytes(int64_t tokens, int64_t experts);
  * What is not there: an expert whose logit or bias is -infinity is never chosen, and a run of such
  * experts neither.  Where a token has fewer than top experts left (a padded token: none), the rest of
  * its slots hold expert -1, weight 0 and place -1.  A key that is NaN counts as +infinity, so that a
- * token of NaN is answered with NaN and not with silence.
+ * token of NaN is answered with NaN and not with silence.  A softmax with NaN or +infinity among its
+ * logits has no scores: the weights of all of the token's experts are NaN.
  *
  * place[t * top + j] is the row of the pair (t, j) when all pairs are sorted by expert and, within an
  * expert, by token; offsets[e] (int64, experts + 1) the row where expert e's start, offsets[experts]

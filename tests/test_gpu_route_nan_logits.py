@@ -27,7 +27,7 @@ def test_route_nan_at_each_expert(g, kind, E, run):  # noqa: F811
         if k > E:
             continue
         print(f"[route] NaN {kind} {E} {run} {k}", flush=True)
-        for renorm in (False, True) if kind == "sigmoid" else (False,):
+        for renorm in (False, True):
             check_route(g, x, k, "f32", kind=kind, bias=bias, renorm=renorm)
         check_route(g, x[:5], k, "bf16", kind=kind, bias=bias)
         check_route(g, np.concatenate([x] * (1 + 70 // len(x))), k, "f16", kind=kind, bias=bias)
@@ -36,3 +36,22 @@ def test_route_nan_at_each_expert(g, kind, E, run):  # noqa: F811
         if E % groups == 0:
             for of in (1, 2):
                 check_route(g, x, min(4, best * E // groups), "f32", kind=kind, bias=bias, groups=groups, best=best, of=of)
+
+
+@pytest.mark.parametrize("E,groups,best", [(8, 1, 1), (16, 4, 2), (60, 1, 1), (256, 8, 3), (512, 1, 1)])
+def test_route_softmax_of_nan_is_not_silent(g, E, groups, best):  # noqa: F811
+    """A softmax over NaN or +infinity has no numbers, so that no expert's weight is one, renormalised or not,
+    also where the expert with the NaN is not among the chosen."""
+    for n in (4, 40, 150):
+        x = logits(n, E, n)
+        for t, (e, v) in enumerate([(E - 1, NAN), (0, NAN), (E // 2, INF)]):
+            x[t, e] = v
+        bias = 0.1 * RNG(E).standard_normal(E)
+        bias[E - 1] = -INF
+        for b, of in ((bias, 1), (bias, 2), (None, 2)):
+            for renorm in (False, True):
+                print(f"[route] NaN softmax {E} {groups} {n} {b is not None} {of} {renorm}", flush=True)
+                with np.errstate(invalid="ignore"):
+                    _, weight, _, _ = check_route(g, x, 2, "f32", kind="softmax", bias=b, groups=groups, best=best, of=of,
+                                                  renorm=renorm)
+                assert np.isnan(weight[:3]).all() and np.isfinite(weight[3:]).all()

@@ -578,7 +578,8 @@ __device__ __forceinline__ float score_near(int sigmoid, float x, float top) {
   return (x > 0.0f ? 1.0f : exp_near(x - fminf(top, 0.0f))) * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
-// Weight of the lane's chosen expert among the token's: p.top lanes hold one each.
+// Weight of the lane's chosen expert among the token's: p.top lanes hold one each.  sum: of the softmax, or any
+// number where nothing but the logits decided the choice (then NaN or +infinity is among the chosen).
 template <int L, int V>
 __device__ __forceinline__ float weight_of(const RouteArgs& p, int chosen, float cx, float x_max, float sum) {
   const bool there = chosen >= 0;
@@ -589,7 +590,10 @@ __device__ __forceinline__ float weight_of(const RouteArgs& p, int chosen, float
   const float top = max_across<L>(there ? (cx != cx ? __builtin_inff() : cx) : kNone);
   float s = score_near(p.score, cx, top);
   if (!there) s = 0.0f;
-  const float all = sum_across<L>(s);
+  float all = sum_across<L>(s);
+  // (a softmax over NaN or +infinity has no scores, also where the chosen logits, which are all that is read
+  // here, are numbers)
+  if (!p.score && sum != sum) all = sum;
   return there ? p.scale * (s / all) : 0.0f;
 }
 
