@@ -86,8 +86,9 @@ GEMM_API gemm_status_t gemm_route(gemm_handle_t h, void* stream, int64_t tokens,
  * logits, score, renorm and scale as gemm_route was given them, expert as it wrote them (the experts of
  * a token are distinct; -1 and any other number that is no expert is skipped); dweight fp32, tokens x
  * top; dlogits: tokens x experts (ldd >= experts) of x_type, computed in fp32 and rounded once.  Every
- * element is written.  A logit of -infinity has gradient 0, also where all of a token's are
- * (but a NaN or +infinity among a softmax's logits makes all of the token's gradients NaN).  Errors as
+ * element is written.  A logit of -infinity has gradient 0, also where all of a token's are.  NaN or
+ * +infinity among the logits of a softmax makes all of the token's gradients NaN; with renorm, where only
+ * the chosen logits are read, those of the chosen if it is one of them, and the others stay 0.  Errors as
  * gemm_route. */
 GEMM_API gemm_status_t gemm_route_grad(gemm_handle_t h, void* stream, int64_t tokens, int64_t experts,
                                        int64_t top, const void* logits, int64_t ldl, gemm_dtype_t x_type,

@@ -5,7 +5,7 @@ Choices, places and offsets have to be equal; the weights' bounds are test_gpu_e
 import numpy as np
 import pytest
 
-from test_gpu_experts import INF, NAN, RNG, check_route, g, logits  # noqa: F401
+from test_gpu_experts import INF, NAN, RNG, call_grad, check_route, g, logits  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +55,34 @@ def test_route_softmax_of_nan_is_not_silent(g, E, groups, best):  # noqa: F811
                     _, weight, _, _ = check_route(g, x, 2, "f32", kind="softmax", bias=b, groups=groups, best=best, of=of,
                                                   renorm=renorm)
                 assert np.isnan(weight[:3]).all() and np.isfinite(weight[3:]).all()
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (60, 4), (200, 16), (300, 6)])
+def test_route_grad_of_nan(g, E, k):  # noqa: F811
+    """What NaN and +infinity among the logits reach: of a softmax as it is every gradient of the token, with
+    renormalisation those of the chosen if it is one of them; of a sigmoid the expert's own, or those of the
+    chosen."""
+    rng = RNG([E, k])
+    n = 20
+    x = logits(n, E, 3)
+    expert = np.argsort(rng.random((n, E)), axis=1)[:, :k]
+    x[1, expert[1, 0]], x[3, expert[3, k - 1]] = NAN, INF
+    free = [next(e for e in range(E) if e not in expert[t]) for t in range(n)]
+    x[5, free[5]], x[7, free[7]] = NAN, INF
+    dw = rng.standard_normal((n, k))
+    chosen = np.zeros((n, E), dtype=bool)
+    chosen[np.arange(n)[:, None], expert] = True
+    for kind in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            got, _ = call_grad(g, x, expert, dw, "f32", kind, renorm, 1.5)
+            want = np.zeros((n, E), dtype=bool)
+            if kind == "softmax" and not renorm:
+                want[[1, 3, 5, 7]] = True
+            elif renorm:
+                want[1] = chosen[1]
+                want[3] = chosen[3] & (kind == "softmax")
+            else:
+                want[1, expert[1, 0]] = True
+            assert np.array_equal(np.isnan(got), want), (kind, renorm)
+            if kind == "sigmoid" or renorm:
+                assert (got[~chosen & ~want] == 0).all()
