@@ -48,8 +48,9 @@ GEMM_API int64_t gemm_route_workspace_bytes(int64_t tokens, int64_t experts);
  *     weight[j] = scale * s[expert[j]],                       or with renorm
  *                 scale * s[expert[j]] / (the sum of the chosen s)
  *
- * The bias decides the choice only.  Keys are compared as if computed in 64 bits; weights are fp32 sums
- * and quotients, within about 2^-21 of the formula.
+ * The bias decides the choice only.  Keys are compared as if computed in 64 bits.  Weights are fp32 sums
+ * and quotients, each within (32 + |x - m|) 2^-24 of itself, x the expert's logit and m the token's largest;
+ * a score under 2^-125 (with renorm, of the largest chosen score) may count as 0.
  *
  * Limited groups: the experts lie in `groups` runs of equal length (groups divides experts, at most
  * 64); a run is worth the sum of its group_top (1 or 2) largest keys (without a bias and with group_top

@@ -561,12 +561,12 @@ __device__ __forceinline__ S softmax_sum(const float (&x)[V], float x_max) {
   }
 }
 
-// exp(v) within two steps: the product with log2(e) in two parts.
+// exp(v) within two steps, 0 below 2^-126: the product with log2(e) in two parts.
 __device__ __forceinline__ float exp_near(float v) {
   constexpr float hi = 1.44269502f, lo = 1.92596299e-8f;  // log2(e) in two fp32 numbers
   const float t = v * hi, rest = fmaf(v, lo, fmaf(v, hi, -t));
   const float e = __builtin_amdgcn_exp2f(t);
-  return fabsf(v) < 80.0f ? fmaf(e, rest * 0.693147181f, e) : e;  // (past that e or the rest may be no number)
+  return fabsf(v) < 87.33f ? fmaf(e, rest * 0.693147181f, e) : e;  // (past 126 ln 2 e or the rest may be no number)
 }
 
 // A chosen score relative to the largest chosen logit, so that their sum is at least 1/2: exp(x - top) for
