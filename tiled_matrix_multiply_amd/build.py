@@ -6,8 +6,9 @@ exported symbols are exactly the C ABI of include/gemm.h, gemm_grouped.h and gem
 Beside it, libgemm_lds_poison.so: the same library with the matrix-core kernels of the main
 families (fp32, fp16, bf16, per-tensor and block-scaled E4M3, E2M1 and E2M3, quantized B, and
 the tiles of the grouped, 8-bit integer and grouped MXFP4 products) built with
-GEMM_DEBUG_POISON_LDS, which fills every LDS stage with all-ones words before it is refilled.
-It is a race check for the staged K loop: its results must equal libgemm.so's bit for bit.
+GEMM_DEBUG_POISON_LDS, which fills every LDS stage, data and block scales, with all-ones words
+before it is refilled.  It is a race check for the staged K loop: its results must equal
+libgemm.so's bit for bit.
 """
 import concurrent.futures as cf
 import os
@@ -26,7 +27,8 @@ POISON_SOURCES = ("mfma_f32.hip", "mfma_f16.hip", "mfma_bf16.hip", "mfma_e4m3.hi
                   "mfma_mx_e4m3.hip", "mfma_e2m1.hip", "mfma_e2m3.hip", "qmfma.hip",
                   "grouped_bf16.hip", "grouped_f16.hip", "grouped_wgrad_bf16.hip",
                   "grouped_wgrad_f16.hip", "grouped_i8_bf16.hip", "grouped_i8_f16.hip",
-                  "grouped_i8_f32.hip", "grouped_mx_bf16.hip")
+                  "grouped_i8_f32.hip", "grouped_mx_bf16.hip", "grouped_mx_f16.hip",
+                  "grouped_mx_f32.hip")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

@@ -1020,7 +1020,7 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, ui
   // value in the 4- and 6-bit ones), between two barriers.  A fragment read of a stage before
   // its copies have landed, or of a tile's stage after its refill began, then reads the poison
   // instead of stale data that may happen to be right, and the result differs from the
-  // library's own.  Only the data stages are poisoned (not the MX scale rows).
+  // library's own.  The MX scale rows likewise (all-ones bytes are NaN scales), chunk by chunk.
   auto poison_stage = [&](int buf) {
     const int gt = tid % (C::NW * 64);
     uint8_t* const a = gsm + OA::LDS_OFF + buf * C::A_BYTES;
@@ -1030,6 +1030,11 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, ui
     for (int o = gt * 16; o < C::B_BYTES; o += C::NW * 64 * 16)
       *reinterpret_cast<u32x4*>(b + o) = u32x4{~0u, ~0u, ~0u, ~0u};
   };
+  auto poison_scales = [&](int c) {
+    if constexpr (C::MX)
+      for (int o = tid * 16; o < C::SC_BUF; o += C::NT * 16)
+        *reinterpret_cast<u32x4*>(smem + C::SC_OFF + (c & 1) * C::SC_BUF + o) = u32x4{~0u, ~0u, ~0u, ~0u};
+  };
 #endif
   auto tile_boundary = [&](int kt, int abuf, int anext) {
     // tiles kt+2 .. min(kt+S-1, KT-1) may stay in flight
@@ -1037,7 +1042,10 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, ui
     if (kt + 2 == KT && need_fix && tile_of(kt + 1) == KT_ALL - 1) fixup(tile_of(kt + 1), anext, anext);
     __syncthreads();
 #ifdef GEMM_DEBUG_POISON_LDS
-    if (kt + C::S < KT) poison_stage(abuf);
+    if (kt + C::S < KT) {
+      poison_stage(abuf);
+      if (C::MX && (kt + C::S) % C::TPC == 0) poison_scales((kt + C::S) / C::TPC);
+    }
     __syncthreads();  // outside the condition: the groups of a split K loop count tiles apart
 #endif
     if (kt + C::S < KT) {  // into the buffers tile kt has released
@@ -1121,6 +1129,8 @@ __device__ __forceinline__ void mfma_tile(const GemmParams p, const SkSeg sg, ui
 #ifdef GEMM_DEBUG_POISON_LDS
 #pragma unroll
   for (int t = 0; t < C::S; ++t) poison_stage(t);
+  poison_scales(0);
+  poison_scales(1);
   __syncthreads();
 #endif
   if constexpr (C::QB != 0) {
