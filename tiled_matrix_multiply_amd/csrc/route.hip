@@ -256,7 +256,14 @@ __device__ __forceinline__ bool keep_run(const RouteArgs& p, int lm, Best2<S> w,
     if (lm > 4) meet(__shfl_xor(w.a, 16), __shfl_xor(w.b, 16));
     if (lm > 5) meet(__shfl_xor(w.a, 32), __shfl_xor(w.b, 32));
   }
-  const S t = p.group_top == 2 && w.b != none ? w.a + w.b : w.a;
+  // Sums of two keys in fp32 are taken in halves: that of two of the type's lowest numbers is a number then, and
+  // not the -infinity of a run without experts.
+  S t = w.a;
+  if (p.group_top == 2) {
+    constexpr S part = EXACT ? (S)1 : (S)0.5;
+    t = part * w.a + (w.b != none ? part * w.b : (S)0);
+    slack *= part;
+  }
   const int first = sub & ~(m - 1);
   int over = 0, near = 0;  // runs that are worth more for certain, and those that may be
   auto rank = [&](S u, int from) {
