@@ -811,8 +811,9 @@ def run_grouped_mx(handle, A, sa, B, sb, C, offsets, *, groups, M, N, K, a_type=
                    beta=0.0, epilogue=GEMM_EPI_NONE, bias=None, lda=None, ldsa=None, ldb=None, ldsb=None,
                    stride_b=None, stride_sb=None, ldc=None, kernel=GEMM_GROUPED_AUTO, stream=None):
     """C[r] = epi(alpha A[r] B_g^T + beta C[r] + bias_g) for the rows r of each group g, with A (M x K) and
-    B_g (N x K) in MXFP4: packed elements, and scale bytes sa and sb (ldsa and ldsb bytes a row).
-    offsets None: one group has all rows.  Raises GemmError on a negative status."""
+    B_g (N x K) in MXFP4: packed elements, and scale bytes sa and sb (ldsa and ldsb bytes a row; multiples
+    of 16 for the tiled kernels, other rows are streamed).  offsets None: one group has all rows.  Raises
+    GemmError on a negative status."""
     ldb = ldb if ldb is not None else K
     ldsb = ldsb if ldsb is not None else K // 32
     st = _lib.gemm_run_grouped_mx(handle, int(kernel), _stream(stream), groups, _ptr(offsets), M, N, K,

@@ -19,8 +19,8 @@
 //
 // What bounds it are chains of dependent steps, not the bytes: the logits' way from memory, `top` maxima across
 // lanes, the counts' way through memory to the second kernel.  One token of 256 experts (sigmoid, bias, 4 of 8
-// groups) 7.0 us, 8191 tokens 17 to 19 (14 and 5.2 by themselves; 8.4 MB, 2 us at the rate of a copy), 16384 of
-// 128 (softmax) 14.0.
+// groups) 7.0 us, 8191 tokens 17 (13.6 and 5.0 by themselves; 8.4 MB, 2 us at the rate of a copy), 16384 of 128
+// (softmax) 14.3.
 #include "experts.hpp"
 #include "grouped.hpp"
 
@@ -855,7 +855,7 @@ __global__ __launch_bounds__(1024) void route_place_kernel(RouteArgs p, int TB, 
 //   dx_e = s_e (g_e - sum_j g_j s_j) = s_e (g_e U + sum_j s_j (g_e - g_j)),   U = the sum of the others' s
 // (g_e = 0 for what was not chosen).  Written as differences none of them cancels where one weight is
 // near 1.
-// Its bytes bound it where there are many tokens: softmax as it is in fp32, 16384 x 128 6.4 us, 16384 x 512 14.0
+// Its bytes bound it where there are many tokens: softmax as it is in fp32, 16384 x 128 6.4 us, 16384 x 512 13.9
 // (4.8 TB/s).
 // A token's row of results lies in LDS between what every expert gets and what the chosen get; only the
 // wave that owns it touches it, so its writes and reads keep their order without a barrier.
